@@ -163,6 +163,17 @@ def _default_stream():
     return None
 
 
+def _current_device():
+    """Index of the device a handle made now belongs to (None without torch or a GPU)."""
+    try:
+        import torch
+        if torch.cuda.is_available():
+            return torch.cuda.current_device()
+    except Exception:
+        pass
+    return None
+
+
 # ---- functions with the C names -------------------------------------------
 
 def signmuon_init(shapes, M, beta, lam, K, eps, scale, P=1, flags=0, stream=None):
@@ -374,7 +385,12 @@ def signmuon_profile_read(h):
     return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(PROF_KINDS)}
 
 
-class SignMuon:
+# the layer calls (include/signmuon_layers.h); layers.py uses the names above
+from .layers import *  # noqa: E402,F401,F403
+from .layers import LayerCalls  # noqa: E402
+
+
+class SignMuon(LayerCalls):
     """Owning wrapper of a handle: ``SignMuon(shapes, M, ...)`` then
     ``.step(W, G, eta)``; the remaining methods mirror the C calls."""
 
@@ -386,6 +402,7 @@ class SignMuon:
         # the CUDA stream the handle enqueues on (a cudaStream_t as an int; 0
         # or None for the legacy default stream)
         self.stream = stream if stream is not None else _default_stream()
+        self.device = _current_device()
         self.h = signmuon_init(self.shapes, M, beta, lam, K, eps, scale, P, flags, self.stream)
         self.info = signmuon_info(self.h)
         self.d = self.info["d"]

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsignmuon.so")
 
 SOURCES = ["kernels_elem.cu", "kernels_ternary.cu", "ns_simt.cu", "ns_tc.cu", "signmuon_api.cu", "noalloc.cu",
-           "plan.cpp"]
+           "layers_embed.cu", "layers_norm.cu", "layers_distill.cu", "layers_api.cu", "plan.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
                      "--expt-relaxed-constexpr"]
@@ -36,7 +36,7 @@ def _nvcc():
 
 
 def _headers():
-    out = [os.path.join(INCLUDE, "signmuon.h")]
+    out = [os.path.join(INCLUDE, f) for f in ("signmuon.h", "signmuon_layers.h")]
     out += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     return out
 

@@ -85,6 +85,11 @@ struct signmuon_ctx {
   cudaEvent_t g_free[2] = {nullptr, nullptr};    // the step that read buffer b is done
   cudaEvent_t w_ready = nullptr;                 // W of the current call is on the device
   cudaEvent_t w_free = nullptr;                  // the previous call's W has gone back
+  // workspace of the layer calls (signmuon_layers.h), as reserved
+  int64_t lay_rows = 0, lay_cols = 0;
+  uint8_t* lay_ws = nullptr;
+  int* lay_status = nullptr;    // [0] an index was out of range; then one row counter per worker, zero between calls
+  int* h_lay_status = nullptr;  // pinned mirror of [0]
   std::vector<void*> allocs;
   int64_t bytes = 0;
   std::string err;

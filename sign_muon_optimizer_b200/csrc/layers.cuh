@@ -1,0 +1,256 @@
+// layers.cuh -- device helpers and launch wrappers of the layer calls
+// (include/signmuon_layers.h): element types, 16-byte strips, the map from
+// work units to workers.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace sm {
+
+enum LayerType { LT_F32 = 0, LT_BF16 = 1, LT_F16 = 2 };
+
+// Rows of each worker, and work units (tiles of rows) that never cross a
+// worker: worker m has rows [start[m], start[m+1]) and units [unit[m],
+// unit[m+1]).  Passed by value (constant bank).
+struct RowMap {
+  int M;
+  int start[kMaxWorkers + 1];
+  int unit[kMaxWorkers + 1];
+};
+
+struct GradPtrs {     // per-worker gradient vectors, passed by value
+  float* p[kMaxWorkers];
+};
+
+#ifdef __CUDACC__
+// the m with pre[m] <= i < pre[m+1] (pre ascending, pre[0] = 0, i < pre[M])
+__device__ __forceinline__ int worker_of(const int* pre, int M, int i) {
+  int lo = 0, hi = M - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+  static constexpr int V = 4;   // elements in 16 bytes
+  static __device__ __forceinline__ float up(float x) { return x; }
+  static __device__ __forceinline__ float down(float x) { return x; }
+};
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
+};
+template <> struct Elem<__half> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
+};
+
+template <typename T>
+struct alignas(16) Pack {
+  T v[Elem<T>::V];
+};
+
+// A strip is what a warp's 32 lanes hold of a row in one step: 32 * V
+// elements.  With VEC a lane holds V neighbours (one 16-byte access; the row
+// starts on 16 bytes and its length is a multiple of V), else element j of the
+// lane is column j * 32 + lane of the strip.
+template <typename T, bool VEC>
+__device__ __forceinline__ int strip_col(int base, int lane, int j) {
+  constexpr int V = Elem<T>::V;
+  return VEC ? base + lane * V + j : base + j * 32 + lane;
+}
+
+// x[j] = row[col], 0 beyond `cols`
+template <typename T, bool VEC>
+__device__ __forceinline__ void strip_load(const T* __restrict__ row, int base, int cols, int lane, float* x) {
+  constexpr int V = Elem<T>::V;
+  if (VEC) {
+    const int c = base + lane * V;
+    Pack<T> p;
+    if (c < cols) p = *reinterpret_cast<const Pack<T>*>(row + c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = c < cols ? Elem<T>::up(p.v[j]) : 0.f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = base + j * 32 + lane;
+      x[j] = c < cols ? Elem<T>::up(row[c]) : 0.f;
+    }
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void strip_store(T* __restrict__ row, int base, int cols, int lane, const float* x) {
+  constexpr int V = Elem<T>::V;
+  if (VEC) {
+    const int c = base + lane * V;
+    if (c < cols) {
+      Pack<T> p;
+#pragma unroll
+      for (int j = 0; j < V; ++j) p.v[j] = Elem<T>::down(x[j]);
+      *reinterpret_cast<Pack<T>*>(row + c) = p;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = base + j * 32 + lane;
+      if (c < cols) row[c] = Elem<T>::down(x[j]);
+    }
+  }
+}
+
+// the strip as it lies in memory (zeros beyond `cols`), to be converted later:
+// half the registers of the values for 16-bit types
+template <typename T, bool VEC>
+__device__ __forceinline__ Pack<T> strip_raw(const T* __restrict__ row, int base, int cols, int lane) {
+  constexpr int V = Elem<T>::V;
+  Pack<T> p;
+  if (VEC) {
+    const int c = base + lane * V;
+    if (c < cols) {
+      p = *reinterpret_cast<const Pack<T>*>(row + c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) p.v[j] = Elem<T>::down(0.f);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = base + j * 32 + lane;
+      p.v[j] = c < cols ? row[c] : Elem<T>::down(0.f);
+    }
+  }
+  return p;
+}
+
+// the fp32 companion of a T strip (a weight, a sum): same columns
+template <typename T, bool VEC>
+__device__ __forceinline__ void strip_load_f32(const float* row, int base, int cols, int lane, float* x) {
+  constexpr int V = Elem<T>::V;
+  if (VEC) {
+    const int c = base + lane * V;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 f = c < cols ? *reinterpret_cast<const float4*>(row + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[j] = f.x; x[j + 1] = f.y; x[j + 2] = f.z; x[j + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = base + j * 32 + lane;
+      x[j] = c < cols ? row[c] : 0.f;
+    }
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void strip_store_f32(float* row, int base, int cols, int lane, const float* x) {
+  constexpr int V = Elem<T>::V;
+  if (VEC) {
+    const int c = base + lane * V;
+    if (c < cols) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4)
+        *reinterpret_cast<float4*>(row + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = base + j * 32 + lane;
+      if (c < cols) row[c] = x[j];
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) {
+  return i64 ? reinterpret_cast<const int64_t*>(ids)[i] : (int64_t)reinterpret_cast<const int32_t*>(ids)[i];
+}
+#endif  // __CUDACC__
+
+// ---- launch wrappers (host) ------------------------------------------------
+constexpr int kEmbTile = 32;     // sorted tokens of one reduction unit: one per lane
+constexpr int kSortTile = 2048;  // tokens sorted by one block
+
+void launch_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const void* ids, int id64, int64_t n,
+                  float scale, void* out, int type, int64_t ld, int* status);
+struct EmbedGradArgs {
+  const void* ids;
+  int id64;
+  int64_t V, E;
+  float scale;
+  const void* dY;
+  int type;
+  int64_t ld;
+  int64_t off;                 // the table's place in G[m]
+  int accumulate;
+  unsigned long long* keys[2]; // workspace: one (id, row) key per row, twice
+  float* part;                 // workspace: 2 x E floats per unit of kEmbTile tokens
+  int* status;
+};
+void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start, int M, const GradPtrs& G);
+
+void launch_layernorm(cudaStream_t s, const float* gamma, const float* beta, int64_t n, int64_t E, const void* X,
+                      int64_t ldx, void* Y, int64_t ldy, int type, float eps, float* mean, float* rstd);
+struct NormGradArgs {
+  const float* gamma;
+  int64_t E;
+  const void* X;
+  int64_t ldx;
+  const void* dY;
+  int64_t ldy;
+  const float* mean;
+  const float* rstd;
+  void* dX;
+  int64_t ldd;
+  int type;
+  int64_t off_gamma, off_beta; // off_beta < 0: none
+  int accumulate;
+  float* part;                 // workspace: 2 x E floats per block
+  int max_blocks;              // blocks that part has room for, at least M
+};
+void launch_layernorm_grad(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G);
+
+struct DistillArgs {
+  const void* Z;
+  int type;
+  int64_t ldz, V;
+  const void* idx;
+  int id64;
+  const void* t;
+  int t_type;
+  int64_t ldt;
+  int K;
+  float temperature, gscale;
+  float* loss;
+  int32_t* count_out;
+  float* row_loss;             // the caller's, or workspace
+  void* dZ;
+  int64_t ldd;
+  int* count;                  // workspace: M counters, zero between calls
+  int* status;
+};
+void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int M);
+
+}  // namespace sm

@@ -585,6 +585,7 @@ void signmuon_destroy(signmuon_t h) {
   for (cudaEvent_t e : h->ev_pool) cudaEventDestroy(e);
   for (void* q : h->allocs) cudaFree(q);
   if (h->h_status) cudaFreeHost(h->h_status);
+  if (h->h_lay_status) cudaFreeHost(h->h_lay_status);
   delete h;
 }
 
