@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsignmuon.so")
 
 SOURCES = ["kernels_elem.cu", "kernels_ternary.cu", "ns_simt.cu", "ns_tc.cu", "signmuon_api.cu", "noalloc.cu",
-           "layers_embed.cu", "layers_norm.cu", "layers_distill.cu", "layers_api.cu", "plan.cpp"]
+           "layers_embed.cu", "layers_norm.cu", "layers_norm_grad.cu", "layers_distill.cu", "layers_api.cu", "plan.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
                      "--expt-relaxed-constexpr"]

@@ -184,6 +184,39 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The compiler must not keep what it derived from these 16 bytes, but derive it
+// again: converted values cost twice the registers of the 16-bit ones.
+template <typename T>
+__device__ __forceinline__ void forget(Pack<T>& p) {
+  uint4& u = reinterpret_cast<uint4&>(p);
+  asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+}
+
+// Asynchronous copies of 16 bytes that only the copying thread reads back:
+// waiting for its own groups is enough, no barrier.  live = false: zeros.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// barrier of the WPR warps that hold a row (group: their number in the block)
+template <int WPR, int WARPS>
+__device__ __forceinline__ void group_sync(int group) {
+  if (WPR == 1) __syncwarp();
+  else if (WPR == WARPS) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(WPR * 32) : "memory");
+}
+
 __device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) {
   return i64 ? reinterpret_cast<const int64_t*>(ids)[i] : (int64_t)reinterpret_cast<const int32_t*>(ids)[i];
 }

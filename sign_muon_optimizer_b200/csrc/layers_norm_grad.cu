@@ -1,0 +1,301 @@
+// layers_norm_grad.cu -- layer norm backward, with the reduction of the
+// weights' gradients per worker.
+#include "layers.cuh"
+
+namespace sm {
+namespace {
+
+constexpr int kStages = 3;
+
+// ---------------------------------------------------------------------------
+// With xh = (X - mean) * rstd and g = dY * gamma, per row
+//   dX = rstd * (g - mean_E(g) - xh * mean_E(g * xh)),
+// and per worker dgamma = sum of dY * xh, dbeta = sum of dY over its rows.
+// Bound by the bytes (X and dY read once, dX written once).  WPR warps hold a
+// row, EPL elements a lane.  A block takes consecutive rows of one worker, so
+// the sums over rows stay in registers, a column per element of a thread; the
+// blocks' sums of each worker are added up in order by k_ln_weights.  Rows on
+// 16-byte boundaries come in through asynchronous copies, kStages rows ahead,
+// into slots that only the copying thread reads, and are read from there in
+// both passes over the row.
+// The longest rows (EPL = 32) leave no registers for the sums and the weights
+// and no shared memory for the slots: their sums are in shared memory, and the
+// second pass loads them again (from L2).
+// ---------------------------------------------------------------------------
+template <typename T, bool VEC, int WPR, int EPL>
+__global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
+    k_ln_bwd(const RowMap map, int rows_per_unit, const T* __restrict__ X, int64_t ldx, const T* dY, int64_t ldy,
+             const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
+             int64_t ldd, int E, float* __restrict__ part) {
+  constexpr int VL = Elem<T>::V;
+  constexpr int CH = EPL / VL;                      // strips per warp
+  constexpr int WARPS = WPR > 8 ? WPR : 8;
+  constexpr int RPB = WARPS / WPR;                  // rows per block at a time
+  constexpr bool WIDE = EPL > 16;
+  constexpr bool RING = VEC && !WIDE;
+  constexpr int COLS = WPR * 32 * EPL;              // columns a row group covers
+  extern __shared__ uint4 dyn[];                    // RING: [kStages][2][CH][threads]; then the sums:
+  float* sums = reinterpret_cast<float*>(dyn);      // WIDE: [2][COLS]; RPB > 1, after the loop: [RPB][COLS]
+  __shared__ float2 buf[2][WARPS];
+  __shared__ float stat[kStages][WARPS][2];
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = warp % WPR, group = warp / WPR;
+  const int m = worker_of(map.unit, map.M, blockIdx.x);
+  const int first = map.start[m] + (blockIdx.x - map.unit[m]) * rows_per_unit;
+  const int last = min(first + rows_per_unit, map.start[m + 1]);
+  const float inv_E = 1.f / (float)E;
+  auto base_of = [&](int c) { return (c * WPR + w) * 32 * VL; };
+  auto fetch = [&](int r, int stage) {
+    if (r < last) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = base_of(c) + lane * VL;
+        const bool in = col < E;
+        uint4* to = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
+        copy16(to, X + (int64_t)r * ldx + (in ? col : 0), in);
+        copy16(to + CH * WARPS * 32, dY + (int64_t)r * ldy + (in ? col : 0), in);
+      }
+      if (lane < 2) copy4(&stat[stage][warp][lane], (lane ? rstd : mean) + r);
+    }
+    copy_commit();
+  };
+  if (RING) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) fetch(first + group + s * RPB, s);
+  }
+  float ga[WIDE ? 1 : CH][VL], ag[WIDE ? 1 : CH][VL], ab[WIDE ? 1 : CH][VL];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    if (!WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, ga[WIDE ? 0 : c]);
+#pragma unroll
+    for (int j = 0; j < VL; ++j) {
+      if (WIDE) {
+        const int col = strip_col<T, VEC>(base_of(c), lane, j);
+        sums[col] = 0.f;
+        sums[COLS + col] = 0.f;
+      } else {
+        ag[WIDE ? 0 : c][j] = 0.f;
+        ab[WIDE ? 0 : c][j] = 0.f;
+      }
+    }
+  }
+  int stage = 0, parity = 0;
+  for (int r = first + group; r < last; r += RPB) {
+    Pack<T> x[WIDE ? 1 : CH], dy[WIDE ? 1 : CH];
+    float mu, rs;
+    if (RING) {
+      copy_wait<kStages - 1>();
+      const float own = lane < 2 ? stat[stage][warp][lane] : 0.f;
+      mu = __shfl_sync(0xffffffffu, own, 0);
+      rs = __shfl_sync(0xffffffffu, own, 1);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint4* from = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
+        x[WIDE ? 0 : c] = *reinterpret_cast<const Pack<T>*>(from);
+        dy[WIDE ? 0 : c] = *reinterpret_cast<const Pack<T>*>(from + CH * WARPS * 32);
+      }
+    } else {
+      mu = mean[r];
+      rs = rstd[r];
+#pragma unroll
+      for (int c = 0; c < CH && !WIDE; ++c) {
+        x[WIDE ? 0 : c] = strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane);
+        dy[WIDE ? 0 : c] = strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane);
+      }
+    }
+    // columns beyond E have dY = 0 and gamma = 0 and add nothing that is kept
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll(WIDE ? 1 : CH)
+    for (int c = 0; c < CH; ++c) {
+      if (base_of(c) >= E) break;
+      float gl[VL];
+      if (WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, gl);
+      const Pack<T> px = WIDE ? strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane) : x[WIDE ? 0 : c];
+      const Pack<T> raw = WIDE ? strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane) : dy[WIDE ? 0 : c];
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const float h = (Elem<T>::up(px.v[j]) - mu) * rs;
+        const float d = Elem<T>::up(raw.v[j]);
+        if (WIDE) {
+          const int col = strip_col<T, VEC>(base_of(c), lane, j);
+          sums[col] = fmaf(d, h, sums[col]);
+          sums[COLS + col] += d;
+        } else {
+          ag[WIDE ? 0 : c][j] = fmaf(d, h, ag[WIDE ? 0 : c][j]);
+          ab[WIDE ? 0 : c][j] += d;
+        }
+        const float g = d * (WIDE ? gl[j] : ga[WIDE ? 0 : c][j]);
+        s1 += g;
+        s2 = fmaf(g, h, s2);
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (WPR > 1) {
+      if (lane == 0) buf[parity][warp] = make_float2(s1, s2);
+      group_sync<WPR, WARPS>(group);
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) {
+        const float2 t = buf[parity][group * WPR + i];
+        s1 += t.x;
+        s2 += t.y;
+      }
+      parity ^= 1;
+    }
+    const float k0 = rs * (s1 * inv_E), k1 = rs * (s2 * inv_E);
+    asm volatile("" ::: "memory");  // the row is read again, not kept in registers as floats
+#pragma unroll(WIDE ? 1 : CH)
+    for (int c = 0; c < CH; ++c) {
+      if (base_of(c) >= E) break;
+      float gl[VL], o[VL];
+      if (WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, gl);
+      Pack<T> px, raw;
+      if (RING) {
+        const uint4* from = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
+        px = *reinterpret_cast<const Pack<T>*>(from);
+        raw = *reinterpret_cast<const Pack<T>*>(from + CH * WARPS * 32);
+      } else {
+        px = WIDE ? strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane) : x[WIDE ? 0 : c];
+        raw = WIDE ? strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane) : dy[WIDE ? 0 : c];
+        forget(px);
+        forget(raw);
+      }
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const float h = (Elem<T>::up(px.v[j]) - mu) * rs;
+        const float g = rs * (WIDE ? gl[j] : ga[WIDE ? 0 : c][j]);
+        o[j] = fmaf(-k1, h, fmaf(Elem<T>::up(raw.v[j]), g, -k0));
+      }
+      strip_store<T, VEC>(dX + (int64_t)r * ldd, base_of(c), E, lane, o);
+    }
+    if (RING) {
+      fetch(r + kStages * RPB, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+  }
+  // the block's sums: row groups added up in order through shared memory
+  float* out = part + (int64_t)blockIdx.x * 2 * E;
+  if (WIDE) {
+    __syncthreads();
+    for (int col = threadIdx.x; col < E; col += WARPS * 32) {
+      out[col] = sums[col];
+      out[E + col] = sums[COLS + col];
+    }
+    return;
+  }
+  if (RING) copy_wait<0>();
+  for (int which = 0; which < 2; ++which) {
+    if (RPB > 1) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const float* v = which ? ab[WIDE ? 0 : c] : ag[WIDE ? 0 : c];
+      if (RPB > 1) strip_store_f32<T, VEC>(sums + group * COLS, base_of(c), COLS, lane, v);
+      else strip_store_f32<T, VEC>(out + which * E, base_of(c), E, lane, v);
+    }
+    if (RPB > 1) {
+      __syncthreads();
+      for (int col = threadIdx.x; col < E; col += WARPS * 32) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < RPB; ++i) t += sums[i * COLS + col];
+        out[which * E + col] = t;
+      }
+    }
+  }
+}
+
+// G[m] (+)= the sum of worker m's blocks, in order: 32 columns a block, 8
+// threads a column, each over a fixed share of the blocks
+__global__ void __launch_bounds__(256) k_ln_weights(const RowMap map, const GradPtrs G, const float* __restrict__ part,
+                                                    int E, int64_t off_gamma, int64_t off_beta, int accumulate) {
+  __shared__ float t[8][33];
+  griddep_wait();
+  griddep_launch();
+  const int m = blockIdx.y;
+  const int which = blockIdx.z;
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  const int u0 = map.unit[m], u1 = map.unit[m + 1];
+  const int share = (u1 - u0 + 7) / 8;
+  float s = 0.f;
+  if (col < E) {
+    const int b = min(u1, u0 + (k + 1) * share);
+#pragma unroll 4
+    for (int u = u0 + k * share; u < b; ++u) s += part[((int64_t)u * 2 + which) * E + col];
+  }
+  t[k][lane] = s;
+  __syncthreads();
+  if (k == 0 && col < E) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += t[i][lane];
+    float* g = G.p[m] + (which ? off_beta : off_gamma) + col;
+    *g = accumulate ? *g + s : s;
+  }
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename T, bool VEC, int WPR, int EPL>
+void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+  constexpr int WARPS = WPR > 8 ? WPR : 8;
+  constexpr int RPB = WARPS / WPR;
+  constexpr int COLS = WPR * 32 * EPL;
+  constexpr bool WIDE = EPL > 16;
+  const size_t ring = VEC && !WIDE ? (size_t)kStages * 2 * (EPL / Elem<T>::V) * WARPS * 32 * 16 : 0;
+  const size_t sums = WIDE ? (size_t)2 * COLS * 4 : (RPB > 1 ? (size_t)RPB * COLS * 4 : 0);
+  const size_t smem = ring > sums ? ring : sums;
+  auto* kernel = k_ln_bwd<T, VEC, WPR, EPL>;
+  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int N = start[M];
+  // one wave of blocks; every worker's rows split into units of equal length
+  int64_t want = (int64_t)num_sms() * resident_per_sm((const void*)kernel, WARPS * 32, smem);
+  if (want > a.max_blocks - M) want = a.max_blocks - M;
+  if (want < 1) want = 1;
+  int64_t per = (N + want - 1) / want;
+  per = (per + RPB - 1) / RPB * RPB;
+  if (per < RPB) per = RPB;
+  RowMap map{};
+  map.M = M;
+  for (int m = 0; m <= M; ++m) map.start[m] = start[m];
+  for (int m = 0; m < M; ++m) map.unit[m + 1] = map.unit[m] + (int)((start[m + 1] - start[m] + per - 1) / per);
+  if (map.unit[M] > 0) {
+    count_launch();
+    launch_pdl(kernel, dim3(map.unit[M]), dim3(WARPS * 32), smem, s, map, (int)per, reinterpret_cast<const T*>(a.X),
+               a.ldx, reinterpret_cast<const T*>(a.dY), a.ldy, a.gamma, a.mean, a.rstd, reinterpret_cast<T*>(a.dX),
+               a.ldd, (int)a.E, a.part);
+  }
+  count_launch();
+  launch_pdl(k_ln_weights, dim3((unsigned)((a.E + 31) / 32), M, a.off_beta >= 0 ? 2 : 1), dim3(256), 0, s, map, G,
+             (const float*)a.part, (int)a.E, a.off_gamma, a.off_beta, a.accumulate);
+}
+
+// the fewest warps that hold a row at 16 elements a lane; beyond 16 warps, 32
+template <typename T, bool VEC>
+void pick_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+  if (a.E <= 256) run_bwd<T, VEC, 1, 8>(s, a, start, M, G);
+  else if (a.E <= 512) run_bwd<T, VEC, 1, 16>(s, a, start, M, G);
+  else if (a.E <= 1024) run_bwd<T, VEC, 2, 16>(s, a, start, M, G);
+  else if (a.E <= 2048) run_bwd<T, VEC, 4, 16>(s, a, start, M, G);
+  else if (a.E <= 4096) run_bwd<T, VEC, 8, 16>(s, a, start, M, G);
+  else if (a.E <= 8192) run_bwd<T, VEC, 16, 16>(s, a, start, M, G);
+  else run_bwd<T, VEC, 16, 32>(s, a, start, M, G);
+}
+
+}  // namespace
+
+void launch_layernorm_grad(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+  const int vl = a.type == LT_F32 ? 4 : 8;
+  const bool vec = a.E % vl == 0 && a.ldx % vl == 0 && a.ldy % vl == 0 && a.ldd % vl == 0 && on16(a.X) && on16(a.dY) &&
+                   on16(a.dX) && on16(a.gamma);
+#define SM_RUN(T) (vec ? pick_bwd<T, true>(s, a, start, M, G) : pick_bwd<T, false>(s, a, start, M, G))
+  if (a.type == LT_F32) SM_RUN(float);
+  else if (a.type == LT_BF16) SM_RUN(__nv_bfloat16);
+  else SM_RUN(__half);
+#undef SM_RUN
+}
+
+}  // namespace sm

@@ -9,6 +9,7 @@ and devices of the tensors and take sizes from them.  Nothing here computes.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 SIGNMUON_F32 = 0
 SIGNMUON_BF16 = 1
@@ -28,14 +29,19 @@ __all__ = EXPORTED_LAYERS + [
     "SIGNMUON_LAYERNORM_MAX_COLS", "SIGNMUON_DISTILL_MAX_K",
 ]
 
-# by the dtype's name: the package itself does not import torch
-_TYPES = {"torch.float32": SIGNMUON_F32, "torch.bfloat16": SIGNMUON_BF16, "torch.float16": SIGNMUON_F16}
-_ID_TYPES = {"torch.int32": SIGNMUON_I32, "torch.int64": SIGNMUON_I64}
+_types = {}     # torch dtype -> type code, filled with the first tensor: the package itself does not import torch
+_id_types = {}
+
+
+def _fill_types():
+    import torch
+    _types.update({torch.float32: SIGNMUON_F32, torch.bfloat16: SIGNMUON_BF16, torch.float16: SIGNMUON_F16})
+    _id_types.update({torch.int32: SIGNMUON_I32, torch.int64: SIGNMUON_I64})
 
 
 def _declare(lib):
     P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
-    PP, PI64 = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_int64)
+    PP = PI64 = P    # addresses of arrays: array.array is several times quicker to make than a ctypes array
     sig = {
         "signmuon_layers_reserve": [P, I64, I64],
         "signmuon_layers_sync": [P],
@@ -57,7 +63,8 @@ _declare(_lib)
 
 
 def _rows_arr(rows):
-    return (ctypes.c_int64 * max(1, len(rows)))(*rows)
+    """Row counts as an array; its address is arr.buffer_info()[0]."""
+    return array("q", rows)
 
 
 # ---- functions with the C names -------------------------------------------
@@ -75,7 +82,8 @@ def signmuon_embed(h, W, mat, ids, id_type, n, scale, out, type, ld):
 
 
 def signmuon_embed_grad(h, mat, ids, id_type, rows, scale, dY, type, ld, G, accumulate):
-    _check(h, _lib.signmuon_embed_grad(h, mat, _ptr(ids), id_type, _rows_arr(rows), scale, _ptr(dY), type, ld,
+    r = _rows_arr(rows)
+    _check(h, _lib.signmuon_embed_grad(h, mat, _ptr(ids), id_type, r.buffer_info()[0], scale, _ptr(dY), type, ld,
                                        _ptr_array(G), accumulate))
 
 
@@ -85,54 +93,77 @@ def signmuon_layernorm(h, W, gamma, beta, n, X, ldx, Y, ldy, type, eps, mean, rs
 
 
 def signmuon_layernorm_grad(h, W, gamma, beta, rows, X, ldx, dY, ldy, mean, rstd, dX, ldd, type, G, accumulate):
-    _check(h, _lib.signmuon_layernorm_grad(h, _ptr(W), gamma, beta, _rows_arr(rows), _ptr(X), ldx, _ptr(dY), ldy,
+    r = _rows_arr(rows)
+    _check(h, _lib.signmuon_layernorm_grad(h, _ptr(W), gamma, beta, r.buffer_info()[0], _ptr(X), ldx, _ptr(dY), ldy,
                                            _ptr(mean), _ptr(rstd), _ptr(dX), ldd, type, _ptr_array(G), accumulate))
 
 
 def signmuon_distill(h, Z, type, ldz, V, idx, id_type, t, t_type, ldt, K, rows, temperature, gscale, loss, count,
                      row_loss, dZ, ldd):
+    r = _rows_arr(rows)
     _check(h, _lib.signmuon_distill(h, _ptr(Z), type, ldz, V, _ptr(idx), id_type, _ptr(t), t_type, ldt, K,
-                                    _rows_arr(rows), temperature, gscale, _ptr(loss), _ptr(count), _ptr(row_loss),
+                                    r.buffer_info()[0], temperature, gscale, _ptr(loss), _ptr(count), _ptr(row_loss),
                                     _ptr(dZ), ldd))
 
 
 # ---- checks of the methods --------------------------------------------------
+# (they run before every launch, so they look at each tensor with few calls)
 
-def _on(opt, name, x):
-    if not hasattr(x, "is_cuda"):
-        raise TypeError(f"{name}: a torch tensor is wanted, got {type(x).__name__}")
-    if not x.is_cuda or x.device.index != opt.device:
-        raise ValueError(f"{name} is on {x.device}, the handle on cuda:{opt.device}")
+def _wrong_device(opt, name, x):
+    if not hasattr(x, "get_device"):
+        return TypeError(f"{name}: a torch tensor is wanted, got {type(x).__name__}")
+    return ValueError(f"{name} is on {x.device}, the handle on cuda:{opt.device}")
 
 
-def _matrix(opt, name, x, n=None, cols=None, dtype=None):
+def _device_of(x):
+    try:
+        return x.get_device()
+    except AttributeError:
+        return None
+
+
+def _matrix(opt, name, x, n=None, cols=None, code=None):
     """Type code and row stride of a 2-D activation with unit column stride."""
-    _on(opt, name, x)
-    code = _TYPES.get(str(x.dtype))
-    if code is None or (dtype is not None and x.dtype != dtype):
-        raise TypeError(f"{name} is {x.dtype}, wanted {dtype or 'float32, bfloat16 or float16'}")
-    if x.dim() != 2 or (n is not None and x.shape[0] != n) or (cols is not None and x.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, wanted ({'rows' if n is None else n}, "
+    if _device_of(x) != opt.device:
+        raise _wrong_device(opt, name, x)
+    if not _types:
+        _fill_types()
+    got = _types.get(x.dtype)
+    if got is None or (code is not None and got != code):
+        raise TypeError(f"{name} is {x.dtype}, wanted float32, bfloat16 or float16, one type for all activations")
+    shape = x.shape
+    if len(shape) != 2 or (n is not None and shape[0] != n) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(shape)}, wanted ({'rows' if n is None else n}, "
                          f"{'columns' if cols is None else cols})")
     ld, one = x.stride()
-    if x.shape[1] > 1 and one != 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
-    if x.shape[0] > 1 and ld < x.shape[1]:
-        raise ValueError(f"{name}: rows overlap (row stride {ld})")
-    return code, max(ld, x.shape[1])
+    if ld < shape[1]:
+        if shape[0] > 1:
+            raise ValueError(f"{name}: rows overlap (row stride {ld})")
+        ld = shape[1]
+    return got, ld
 
 
-def _vector(opt, name, x, n, dtype="torch.float32"):
-    _on(opt, name, x)
-    if str(x.dtype) != dtype:
-        raise TypeError(f"{name} is {x.dtype}, wanted {dtype}")
+def _vector(opt, name, x, n, integer=False):
+    """The address of n adjacent float32 (or int32) elements."""
+    if _device_of(x) != opt.device:
+        raise _wrong_device(opt, name, x)
+    if not _types:
+        _fill_types()
+    if (_id_types if integer else _types).get(x.dtype) != 0:
+        raise TypeError(f"{name} is {x.dtype}, wanted {'int32' if integer else 'float32'}")
     if x.numel() < n or not x.is_contiguous():
         raise ValueError(f"{name}: {n} adjacent elements are wanted, got shape {tuple(x.shape)}, strides {x.stride()}")
+    return x.data_ptr()
 
 
 def _id_type(opt, name, x):
-    _on(opt, name, x)
-    code = _ID_TYPES.get(str(x.dtype))
+    if _device_of(x) != opt.device:
+        raise _wrong_device(opt, name, x)
+    if not _types:
+        _fill_types()
+    code = _id_types.get(x.dtype)
     if code is None:
         raise TypeError(f"{name} is {x.dtype}, wanted int32 or int64")
     return code
@@ -150,17 +181,24 @@ def _share(opt, rows, n):
     if rows is None:
         if n % opt.M:
             raise ValueError(f"{n} rows do not split evenly over {opt.M} workers: give rows")
-        return [n // opt.M] * opt.M
-    if len(rows) != opt.M or sum(rows) != n:
+        rows = [n // opt.M] * opt.M
+    elif len(rows) != opt.M or sum(rows) != n:
         raise ValueError(f"rows must be {opt.M} counts that add up to {n}, got {list(rows)}")
-    return rows
+    return array("q", rows)
 
 
 def _grads(opt, G):
+    """Addresses of the M gradient vectors."""
     if len(G) != opt.M:
         raise ValueError(f"G has {len(G)} vectors, wanted one for each of {opt.M} workers")
-    for m, g in enumerate(G):
-        _vector(opt, "G[%d]" % m, g, opt.d)
+    if not _types:
+        _fill_types()
+    device, d, at = opt.device, opt.d, []
+    for g in G:
+        if _device_of(g) != device or _types.get(g.dtype) != SIGNMUON_F32 or g.numel() < d or not g.is_contiguous():
+            _vector(opt, "G[m]", g, d)   # says which
+        at.append(g.data_ptr())
+    return array("Q", at)
 
 
 def _mat(opt, name, mat):
@@ -184,18 +222,23 @@ class LayerCalls:
     def embed(self, W, mat, ids, out, scale=1.0):
         """out[r] = scale * W[mat][ids[r]]; a negative id gives a row of zeros."""
         cols = _mat(self, "mat", mat)[1]
-        _vector(self, "W", W, self.d)
+        w = _vector(self, "W", W, self.d)
         id_type, n = _ids(self, "ids", ids)
         code, ld = _matrix(self, "out", out, n, cols)
-        signmuon_embed(self.h, W, mat, ids, id_type, n, scale, out, code, ld)
+        rc = _lib.signmuon_embed(self.h, w, mat, ids.data_ptr(), id_type, n, scale, out.data_ptr(), code, ld)
+        if rc:
+            _check(self.h, rc)
 
     def embed_grad(self, mat, ids, dY, G, rows=None, scale=1.0, accumulate=False):
         """G[m][mat][v] = scale * sum of dY[r] over worker m's rows with ids[r] = v."""
         cols = _mat(self, "mat", mat)[1]
         id_type, n = _ids(self, "ids", ids)
         code, ld = _matrix(self, "dY", dY, n, cols)
-        _grads(self, G)
-        signmuon_embed_grad(self.h, mat, ids, id_type, _share(self, rows, n), scale, dY, code, ld, G, bool(accumulate))
+        r, g = _share(self, rows, n), _grads(self, G)
+        rc = _lib.signmuon_embed_grad(self.h, mat, ids.data_ptr(), id_type, r.buffer_info()[0], scale, dY.data_ptr(),
+                                      code, ld, g.buffer_info()[0], bool(accumulate))
+        if rc:
+            _check(self.h, rc)
 
     def _norm_cols(self, gamma, beta):
         r, c = _mat(self, "gamma", gamma)
@@ -206,29 +249,32 @@ class LayerCalls:
     def layernorm(self, W, gamma, beta, X, Y, mean=None, rstd=None, eps=1e-5):
         """Y = (X - mean) * rstd * W[gamma] + W[beta]; beta may be None."""
         cols = self._norm_cols(gamma, beta)
-        _vector(self, "W", W, self.d)
+        w = _vector(self, "W", W, self.d)
         code, ldx = _matrix(self, "X", X, None, cols)
         n = X.shape[0]
-        _, ldy = _matrix(self, "Y", Y, n, cols, X.dtype)
-        if mean is not None:
-            _vector(self, "mean", mean, n)
-        if rstd is not None:
-            _vector(self, "rstd", rstd, n)
-        signmuon_layernorm(self.h, W, gamma, -1 if beta is None else beta, n, X, ldx, Y, ldy, code, eps, mean, rstd)
+        _, ldy = _matrix(self, "Y", Y, n, cols, code)
+        mean = None if mean is None else _vector(self, "mean", mean, n)
+        rstd = None if rstd is None else _vector(self, "rstd", rstd, n)
+        rc = _lib.signmuon_layernorm(self.h, w, gamma, -1 if beta is None else beta, n, X.data_ptr(), ldx, Y.data_ptr(),
+                                     ldy, code, eps, mean, rstd)
+        if rc:
+            _check(self.h, rc)
 
     def layernorm_grad(self, W, gamma, beta, X, dY, mean, rstd, dX, G, rows=None, accumulate=False):
         """dX, and per worker the gradients of W[gamma] and W[beta] in G[m]."""
         cols = self._norm_cols(gamma, beta)
-        _vector(self, "W", W, self.d)
+        w = _vector(self, "W", W, self.d)
         code, ldx = _matrix(self, "X", X, None, cols)
         n = X.shape[0]
-        _, ldy = _matrix(self, "dY", dY, n, cols, X.dtype)
-        _, ldd = _matrix(self, "dX", dX, n, cols, X.dtype)
-        _vector(self, "mean", mean, n)
-        _vector(self, "rstd", rstd, n)
-        _grads(self, G)
-        signmuon_layernorm_grad(self.h, W, gamma, -1 if beta is None else beta, _share(self, rows, n), X, ldx, dY, ldy,
-                                mean, rstd, dX, ldd, code, G, bool(accumulate))
+        _, ldy = _matrix(self, "dY", dY, n, cols, code)
+        _, ldd = _matrix(self, "dX", dX, n, cols, code)
+        r, g = _share(self, rows, n), _grads(self, G)
+        rc = _lib.signmuon_layernorm_grad(self.h, w, gamma, -1 if beta is None else beta, r.buffer_info()[0],
+                                          X.data_ptr(), ldx, dY.data_ptr(), ldy, _vector(self, "mean", mean, n),
+                                          _vector(self, "rstd", rstd, n), dX.data_ptr(), ldd, code, g.buffer_info()[0],
+                                          bool(accumulate))
+        if rc:
+            _check(self.h, rc)
 
     def distill(self, Z, idx, t, loss, rows=None, count=None, row_loss=None, dZ=None, temperature=1.0, gscale=1.0):
         """Distillation loss per worker from the teacher's entries (idx, t) and,
@@ -241,13 +287,15 @@ class LayerCalls:
         if idx.shape != t.shape or (n > 1 and idx.stride(0) != t.stride(0)) or (K > 1 and idx.stride(1) != 1):
             raise ValueError(f"idx (shape {tuple(idx.shape)}, strides {idx.stride()}) must be laid out like t "
                              f"(shape {tuple(t.shape)}, strides {t.stride()})")
-        _vector(self, "loss", loss, self.M)
-        if count is not None:
-            _vector(self, "count", count, self.M, "torch.int32")
-        if row_loss is not None:
-            _vector(self, "row_loss", row_loss, n)
-        ldd = V
+        to = _vector(self, "loss", loss, self.M)
+        count = None if count is None else _vector(self, "count", count, self.M, True)
+        row_loss = None if row_loss is None else _vector(self, "row_loss", row_loss, n)
+        grad, ldd = None, V
         if dZ is not None:
-            _, ldd = _matrix(self, "dZ", dZ, n, V, Z.dtype)
-        signmuon_distill(self.h, Z, code, ldz, V, idx, id_type, t, t_code, ldt, K, _share(self, rows, n), temperature,
-                         gscale, loss, count, row_loss, dZ, ldd)
+            ldd = _matrix(self, "dZ", dZ, n, V, code)[1]
+            grad = dZ.data_ptr()
+        r = _share(self, rows, n)
+        rc = _lib.signmuon_distill(self.h, Z.data_ptr(), code, ldz, V, idx.data_ptr(), id_type, t.data_ptr(), t_code, ldt,
+                                   K, r.buffer_info()[0], temperature, gscale, to, count, row_loss, grad, ldd)
+        if rc:
+            _check(self.h, rc)
