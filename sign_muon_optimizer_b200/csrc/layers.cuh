@@ -184,12 +184,37 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// The compiler must not keep what it derived from these 16 bytes, but derive it
-// again: converted values cost twice the registers of the 16-bit ones.
-template <typename T>
-__device__ __forceinline__ void forget(Pack<T>& p) {
-  uint4& u = reinterpret_cast<uint4&>(p);
-  asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+// Pairs of fp32 operations in one instruction: the kernels over rows are bound
+// by the instructions they issue as much as by the bytes.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  const float2 f = unpack2(a);
+  return f.x + f.y;
 }
 
 // Asynchronous copies of 16 bytes that only the copying thread reads back:

@@ -47,14 +47,21 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
 #pragma unroll
     for (int s = 0; s < kStages; ++s) fetch(r_first + s * step, s);
   }
-  float g[KEEP ? CH : 1][VL], b[KEEP ? CH : 1][VL];
-  auto weights = [&](int c, float* gc, float* bc) {
-    strip_load_f32<T, VEC>(gamma, (c * WPR + w) * 32 * VL, E, lane, gc);
+  // pairs of columns: the weights of this thread's columns
+  F2 g[KEEP ? CH : 1][VL / 2], b[KEEP ? CH : 1][VL / 2];
+  auto load_pairs = [&](const float* from, int c, F2* to) {
+    float t[VL];
+    strip_load_f32<T, VEC>(from, (c * WPR + w) * 32 * VL, E, lane, t);
+#pragma unroll
+    for (int j = 0; j < VL / 2; ++j) to[j] = pack2(t[2 * j], t[2 * j + 1]);
+  };
+  auto weights = [&](int c, F2* gc, F2* bc) {
+    load_pairs(gamma, c, gc);
     if (beta != nullptr) {
-      strip_load_f32<T, VEC>(beta, (c * WPR + w) * 32 * VL, E, lane, bc);
+      load_pairs(beta, c, bc);
     } else {
 #pragma unroll
-      for (int j = 0; j < VL; ++j) bc[j] = 0.f;
+      for (int j = 0; j < VL / 2; ++j) bc[j] = 0ull;
     }
   };
   if (KEEP) {
@@ -63,26 +70,24 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
   }
   int stage = 0;
   for (int64_t r = r_first; r < n; r += step) {
-    float x[CH][VL];
-    float s = 0.f;
-    if (VEC) {
-      copy_wait<kStages - 1>();
+    F2 x[CH][VL / 2];
+    if (VEC) copy_wait<kStages - 1>();
+    F2 a = 0ull;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const Pack<T> p = *reinterpret_cast<const Pack<T>*>(&ring[(stage * CH + c) * (WARPS * 32) + threadIdx.x]);
+    for (int c = 0; c < CH; ++c) {
+      Pack<T> p;
+      if (VEC) p = *reinterpret_cast<const Pack<T>*>(&ring[(stage * CH + c) * (WARPS * 32) + threadIdx.x]);
+      else p = strip_raw<T, VEC>(X + r * ldx, (c * WPR + w) * 32 * VL, E, lane);
 #pragma unroll
-        for (int j = 0; j < VL; ++j) x[c][j] = Elem<T>::up(p.v[j]);
+      for (int j = 0; j < VL / 2; ++j) {
+        x[c][j] = pack2(Elem<T>::up(p.v[2 * j]), Elem<T>::up(p.v[2 * j + 1]));
+        a = add2(x[c][j], a);
       }
+    }
+    if (VEC) {
       fetch(r + kStages * step, stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) strip_load<T, VEC>(X + r * ldx, (c * WPR + w) * 32 * VL, E, lane, x[c]);
     }
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < VL; ++j) s += x[c][j];
     auto row_sum = [&](float v, float* at) {
       v = warp_sum(v);
       if (WPR == 1) return v;
@@ -93,30 +98,41 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
       for (int i = 0; i < WPR; ++i) t += at[group * WPR + i];
       return t;
     };
-    const float mu = row_sum(s, buf[0]) * inv_E;
-    s = 0.f;
+    const float mu = row_sum(sum2(a), buf[0]) * inv_E;
+    const F2 neg_mu = pack2(-mu, -mu);
+    a = 0ull;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      const int base = (c * WPR + w) * 32 * VL;
 #pragma unroll
-      for (int j = 0; j < VL; ++j) {
-        // (columns beyond E were loaded as zeros and must not count)
-        const float d = strip_col<T, VEC>((c * WPR + w) * 32 * VL, lane, j) < E ? x[c][j] - mu : 0.f;
-        x[c][j] = d;
-        s = fmaf(d, d, s);
+      for (int j = 0; j < VL / 2; ++j) {
+        x[c][j] = add2(x[c][j], neg_mu);
+        if (base + 32 * VL > E) {  // columns beyond E were loaded as zeros and must not count
+          const float2 t = unpack2(x[c][j]);
+          x[c][j] = pack2(strip_col<T, VEC>(base, lane, 2 * j) < E ? t.x : 0.f,
+                          strip_col<T, VEC>(base, lane, 2 * j + 1) < E ? t.y : 0.f);
+        }
+        a = fma2(x[c][j], x[c][j], a);
       }
     }
-    const float rs = 1.f / sqrtf(row_sum(s, buf[1]) * inv_E + eps);
+    const float rs = 1.f / sqrtf(row_sum(sum2(a), buf[1]) * inv_E + eps);
     if (mean != nullptr && w == 0 && lane == 0) {
       mean[r] = mu;
       rstd[r] = rs;
     }
+    const F2 rs2 = pack2(rs, rs);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int base = (c * WPR + w) * 32 * VL;
       if (!KEEP) weights(c, g[0], b[0]);
+      float o[VL];
 #pragma unroll
-      for (int j = 0; j < VL; ++j) x[c][j] = fmaf(x[c][j] * rs, g[KEEP ? c : 0][j], b[KEEP ? c : 0][j]);
-      strip_store<T, VEC>(Y + r * ldy, base, E, lane, x[c]);
+      for (int j = 0; j < VL / 2; ++j) {
+        const float2 t = unpack2(fma2(mul2(x[c][j], rs2), g[KEEP ? c : 0][j], b[KEEP ? c : 0][j]));
+        o[2 * j] = t.x;
+        o[2 * j + 1] = t.y;
+      }
+      strip_store<T, VEC>(Y + r * ldy, base, E, lane, o);
     }
   }
 }

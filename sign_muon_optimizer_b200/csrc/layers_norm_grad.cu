@@ -16,8 +16,7 @@ constexpr int kStages = 3;
 // the sums over rows stay in registers, a column per element of a thread; the
 // blocks' sums of each worker are added up in order by k_ln_weights.  Rows on
 // 16-byte boundaries come in through asynchronous copies, kStages rows ahead,
-// into slots that only the copying thread reads, and are read from there in
-// both passes over the row.
+// into slots that only the copying thread reads.
 // The longest rows (EPL = 32) leave no registers for the sums and the weights
 // and no shared memory for the slots: their sums are in shared memory, and the
 // second pass loads them again (from L2).
@@ -65,74 +64,102 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
 #pragma unroll
     for (int s = 0; s < kStages; ++s) fetch(first + group + s * RPB, s);
   }
-  float ga[WIDE ? 1 : CH][VL], ag[WIDE ? 1 : CH][VL], ab[WIDE ? 1 : CH][VL];
+  // pairs of columns: the weights and the sums of this thread's columns
+  constexpr int CK = WIDE ? 1 : CH;
+  F2 ga[CK][VL / 2], ag[CK][VL / 2], ab[CK][VL / 2];
+  auto load_gamma = [&](int c, F2* to) {
+    float t[VL];
+    strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, t);
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    if (!WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, ga[WIDE ? 0 : c]);
+    for (int j = 0; j < VL / 2; ++j) to[j] = pack2(t[2 * j], t[2 * j + 1]);
+  };
+  if (WIDE) {
+    for (int i = threadIdx.x; i < 2 * COLS; i += WARPS * 32) sums[i] = 0.f;
+    __syncthreads();
+  } else {
 #pragma unroll
-    for (int j = 0; j < VL; ++j) {
-      if (WIDE) {
-        const int col = strip_col<T, VEC>(base_of(c), lane, j);
-        sums[col] = 0.f;
-        sums[COLS + col] = 0.f;
-      } else {
-        ag[WIDE ? 0 : c][j] = 0.f;
-        ab[WIDE ? 0 : c][j] = 0.f;
-      }
+    for (int c = 0; c < CK; ++c) {
+      load_gamma(c, ga[c]);
+#pragma unroll
+      for (int j = 0; j < VL / 2; ++j) ag[c][j] = ab[c][j] = 0ull;
     }
   }
   int stage = 0, parity = 0;
   for (int r = first + group; r < last; r += RPB) {
-    Pack<T> x[WIDE ? 1 : CH], dy[WIDE ? 1 : CH];
+    const T* xr = X + (int64_t)r * ldx;
+    const T* dr = dY + (int64_t)r * ldy;
     float mu, rs;
     if (RING) {
       copy_wait<kStages - 1>();
       const float own = lane < 2 ? stat[stage][warp][lane] : 0.f;
       mu = __shfl_sync(0xffffffffu, own, 0);
       rs = __shfl_sync(0xffffffffu, own, 1);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint4* from = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
-        x[WIDE ? 0 : c] = *reinterpret_cast<const Pack<T>*>(from);
-        dy[WIDE ? 0 : c] = *reinterpret_cast<const Pack<T>*>(from + CH * WARPS * 32);
-      }
     } else {
       mu = mean[r];
       rs = rstd[r];
-#pragma unroll
-      for (int c = 0; c < CH && !WIDE; ++c) {
-        x[WIDE ? 0 : c] = strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane);
-        dy[WIDE ? 0 : c] = strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane);
-      }
     }
-    // columns beyond E have dY = 0 and gamma = 0 and add nothing that is kept
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll(WIDE ? 1 : CH)
-    for (int c = 0; c < CH; ++c) {
-      if (base_of(c) >= E) break;
-      float gl[VL];
-      if (WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, gl);
-      const Pack<T> px = WIDE ? strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane) : x[WIDE ? 0 : c];
-      const Pack<T> raw = WIDE ? strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane) : dy[WIDE ? 0 : c];
+    const F2 neg_mu = pack2(-mu, -mu), rs2 = pack2(rs, rs);
+    // xh and rs * g of this thread's columns; both are 0 times what is kept
+    // in columns beyond E, where dY and gamma were loaded as zeros
+    F2 h[CK][VL / 2], g[CK][VL / 2];
+    auto convert = [&](int c, F2* hc, F2* gc, F2* dc, const F2* gamma_c) {
+      Pack<T> px, pd;
+      if (RING) {
+        const uint4* from = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
+        px = *reinterpret_cast<const Pack<T>*>(from);
+        pd = *reinterpret_cast<const Pack<T>*>(from + CH * WARPS * 32);
+      } else {
+        px = strip_raw<T, VEC>(xr, base_of(c), E, lane);
+        pd = strip_raw<T, VEC>(dr, base_of(c), E, lane);
+      }
 #pragma unroll
-      for (int j = 0; j < VL; ++j) {
-        const float h = (Elem<T>::up(px.v[j]) - mu) * rs;
-        const float d = Elem<T>::up(raw.v[j]);
-        if (WIDE) {
-          const int col = strip_col<T, VEC>(base_of(c), lane, j);
-          sums[col] = fmaf(d, h, sums[col]);
-          sums[COLS + col] += d;
-        } else {
-          ag[WIDE ? 0 : c][j] = fmaf(d, h, ag[WIDE ? 0 : c][j]);
-          ab[WIDE ? 0 : c][j] += d;
+      for (int j = 0; j < VL / 2; ++j) {
+        const F2 x = pack2(Elem<T>::up(px.v[2 * j]), Elem<T>::up(px.v[2 * j + 1]));
+        dc[j] = pack2(Elem<T>::up(pd.v[2 * j]), Elem<T>::up(pd.v[2 * j + 1]));
+        hc[j] = mul2(add2(x, neg_mu), rs2);
+        gc[j] = mul2(dc[j], gamma_c[j]);
+      }
+    };
+    F2 a1 = 0ull, a2 = 0ull;   // sums of g and g * xh
+    if (!WIDE) {
+#pragma unroll
+      for (int c = 0; c < CK; ++c) {
+        if (base_of(c) >= E) continue;
+        F2 d[VL / 2];
+        convert(c, h[c], g[c], d, ga[c]);
+#pragma unroll
+        for (int j = 0; j < VL / 2; ++j) {
+          ag[c][j] = fma2(d[j], h[c][j], ag[c][j]);
+          ab[c][j] = add2(d[j], ab[c][j]);
+          a1 = add2(g[c][j], a1);
+          a2 = fma2(g[c][j], h[c][j], a2);
         }
-        const float g = d * (WIDE ? gl[j] : ga[WIDE ? 0 : c][j]);
-        s1 += g;
-        s2 = fmaf(g, h, s2);
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < CH; ++c) {
+        if (base_of(c) >= E) continue;
+        F2 d[VL / 2];
+        load_gamma(c, ga[0]);
+        convert(c, h[0], g[0], d, ga[0]);
+#pragma unroll
+        for (int j = 0; j < VL / 2; ++j) {
+          const float2 p = unpack2(mul2(d[j], h[0][j])), q = unpack2(d[j]);
+          const int c0 = strip_col<T, VEC>(base_of(c), lane, 2 * j), c1 = strip_col<T, VEC>(base_of(c), lane, 2 * j + 1);
+          sums[c0] += p.x;
+          sums[c1] += p.y;
+          sums[COLS + c0] += q.x;
+          sums[COLS + c1] += q.y;
+          a1 = add2(g[0][j], a1);
+          a2 = fma2(g[0][j], h[0][j], a2);
+        }
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    if (RING) {
+      fetch(r + kStages * RPB, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    float s1 = warp_sum(sum2(a1)), s2 = warp_sum(sum2(a2));
     if (WPR > 1) {
       if (lane == 0) buf[parity][warp] = make_float2(s1, s2);
       group_sync<WPR, WARPS>(group);
@@ -145,35 +172,24 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
       }
       parity ^= 1;
     }
-    const float k0 = rs * (s1 * inv_E), k1 = rs * (s2 * inv_E);
-    asm volatile("" ::: "memory");  // the row is read again, not kept in registers as floats
+    const float k0 = -rs * (s1 * inv_E), k1 = -rs * (s2 * inv_E);
+    const F2 k02 = pack2(k0, k0), k12 = pack2(k1, k1);
 #pragma unroll(WIDE ? 1 : CH)
     for (int c = 0; c < CH; ++c) {
-      if (base_of(c) >= E) break;
-      float gl[VL], o[VL];
-      if (WIDE) strip_load_f32<T, VEC>(gamma, base_of(c), E, lane, gl);
-      Pack<T> px, raw;
-      if (RING) {
-        const uint4* from = &dyn[(stage * 2 * CH + c) * (WARPS * 32) + threadIdx.x];
-        px = *reinterpret_cast<const Pack<T>*>(from);
-        raw = *reinterpret_cast<const Pack<T>*>(from + CH * WARPS * 32);
-      } else {
-        px = WIDE ? strip_raw<T, VEC>(X + (int64_t)r * ldx, base_of(c), E, lane) : x[WIDE ? 0 : c];
-        raw = WIDE ? strip_raw<T, VEC>(dY + (int64_t)r * ldy, base_of(c), E, lane) : dy[WIDE ? 0 : c];
-        forget(px);
-        forget(raw);
+      if (base_of(c) >= E) continue;
+      if (WIDE) {
+        F2 d[VL / 2];
+        load_gamma(c, ga[0]);
+        convert(c, h[0], g[0], d, ga[0]);
       }
+      float o[VL];
 #pragma unroll
-      for (int j = 0; j < VL; ++j) {
-        const float h = (Elem<T>::up(px.v[j]) - mu) * rs;
-        const float g = rs * (WIDE ? gl[j] : ga[WIDE ? 0 : c][j]);
-        o[j] = fmaf(-k1, h, fmaf(Elem<T>::up(raw.v[j]), g, -k0));
+      for (int j = 0; j < VL / 2; ++j) {
+        const float2 t = unpack2(fma2(k12, h[WIDE ? 0 : c][j], fma2(rs2, g[WIDE ? 0 : c][j], k02)));
+        o[2 * j] = t.x;
+        o[2 * j + 1] = t.y;
       }
       strip_store<T, VEC>(dX + (int64_t)r * ldd, base_of(c), E, lane, o);
-    }
-    if (RING) {
-      fetch(r + kStages * RPB, stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
   }
   // the block's sums: row groups added up in order through shared memory
@@ -191,7 +207,13 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
     if (RPB > 1) __syncthreads();
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const float* v = which ? ab[WIDE ? 0 : c] : ag[WIDE ? 0 : c];
+      float v[VL];
+#pragma unroll
+      for (int j = 0; j < VL / 2; ++j) {
+        const float2 t = unpack2(which ? ab[WIDE ? 0 : c][j] : ag[WIDE ? 0 : c][j]);
+        v[2 * j] = t.x;
+        v[2 * j + 1] = t.y;
+      }
       if (RPB > 1) strip_store_f32<T, VEC>(sums + group * COLS, base_of(c), COLS, lane, v);
       else strip_store_f32<T, VEC>(out + which * E, base_of(c), E, lane, v);
     }
