@@ -53,7 +53,7 @@ extern "C" {
  * up to max_cols entries.  Call it once after signmuon_init; a later call
  * with larger sizes allocates a larger workspace and keeps the old one until
  * signmuon_destroy (graphs captured before stay valid).  Waits for the
- * handle's stream; not during capture.  1 <= max_rows, max_cols < 2^31.
+ * handle's stream; not during capture.  1 <= max_rows, max_cols <= 2^30.
  * Errors: E_INVALID, E_NOMEM, E_CUDA.  The calls below return E_UNSUPPORTED
  * before it, and E_INVALID where they need more than was reserved.
  * ---------------------------------------------------------------------- */
@@ -71,7 +71,7 @@ int signmuon_layers_sync(signmuon_t h);
  * signmuon_embed -- out[r] = scale * W[mat][ids[r]], r < n.
  *   W     device float[d].   mat: a V x E table.
  *   ids   device int32/int64[n]; a negative id (padding) gives a row of zeros.
- *   out   n x E, row stride ld.
+ *   out   n x E, row stride ld.  0 <= n <= 2^30, E <= 2^30.
  * ---------------------------------------------------------------------- */
 int signmuon_embed(signmuon_t h, const float* W, int mat, const void* ids, int id_type, int64_t n,
                    float scale, void* out, int type, int64_t ld);
@@ -94,7 +94,7 @@ int signmuon_embed_grad(signmuon_t h, int mat, const void* ids, int id_type, con
  * signmuon_layernorm -- Y = (X - mean) * rstd * gamma + beta per row, with
  * mean = sum X / E and rstd = 1 / sqrt(sum (X - mean)^2 / E + eps).
  *   gamma, beta  matrices with E = rows*cols entries each; beta = -1: none.
- *   n, X, Y      n x E, row strides ldx, ldy, both of `type`.
+ *   n, X, Y      n x E, row strides ldx, ldy, both of `type`; 0 <= n <= 2^30.
  *   mean, rstd   device float[n], what signmuon_layernorm_grad reads; may be
  *                NULL (both).
  * eps > 0.  The statistics are held in fp32; the variance is summed around

@@ -248,7 +248,7 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) 
 #endif  // __CUDACC__
 
 // ---- launch wrappers (host) ------------------------------------------------
-constexpr int kEmbTile = 32;     // sorted tokens of one reduction unit: one per lane
+constexpr int kEmbUnit = 256;    // sorted tokens of one block of the reduction
 constexpr int kSortTile = 2048;  // tokens sorted by one block
 
 void launch_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const void* ids, int id64, int64_t n,
@@ -264,7 +264,7 @@ struct EmbedGradArgs {
   int64_t off;                 // the table's place in G[m]
   int accumulate;
   unsigned long long* keys[2]; // workspace: one (id, row) key per row, twice
-  float* part;                 // workspace: 2 x E floats per unit of kEmbTile tokens
+  float* part;                 // workspace: 2 x E floats per unit of kEmbUnit tokens
   int* status;
 };
 void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start, int M, const GradPtrs& G);

@@ -99,6 +99,9 @@ int check_grads(signmuon_t h, float* const* G, sm::GradPtrs* out) {
     if (rc_ != SIGNMUON_OK) return rc_; \
   } while (0)
 
+// rows of a call, and entries of a table's row: leaves room in 32-bit indices
+constexpr int64_t kMaxSize = int64_t(1) << 30;
+
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // blocks of the layer norm backward pass: at most 8 per SM, and one more per
@@ -107,7 +110,7 @@ int norm_blocks(signmuon_t h) { return h->n_sm * 8 + h->M; }
 
 // workspace layout, in bytes: embed_grad has two key arrays and the parts of
 // cut runs, layernorm_grad the blocks' sums, distill the rows' losses
-int64_t embed_units(signmuon_t h, int64_t rows) { return rows / sm::kEmbTile + h->M + 1; }
+int64_t embed_units(signmuon_t h, int64_t rows) { return rows / sm::kEmbUnit + h->M + 1; }
 int64_t embed_bytes(signmuon_t h, int64_t rows, int64_t cols) {
   return 2 * align256(rows * 8) + embed_units(h, rows) * 2 * cols * 4;
 }
@@ -123,8 +126,8 @@ int signmuon_layers_reserve(signmuon_t h, int64_t max_rows, int64_t max_cols) {
   return guarded([&]() -> int {
     DeviceGuard dev_guard(h);
     TRY(check_handle(h, false));
-    if (max_rows < 1 || max_rows > INT_MAX || max_cols < 1 || max_cols > INT_MAX)
-      return fail(h, SIGNMUON_E_INVALID, "max_rows and max_cols must be in [1, 2^31)");
+    if (max_rows < 1 || max_rows > kMaxSize || max_cols < 1 || max_cols > kMaxSize)
+      return fail(h, SIGNMUON_E_INVALID, "max_rows and max_cols must be in [1, 2^30]");
     if (max_rows <= h->lay_rows && max_cols <= h->lay_cols) return SIGNMUON_OK;
     if (max_rows < h->lay_rows) max_rows = h->lay_rows;
     if (max_cols < h->lay_cols) max_cols = h->lay_cols;
@@ -169,9 +172,10 @@ int signmuon_embed(signmuon_t h, const float* W, int mat, const void* ids, int i
     TRY(ready(h));
     TRY(check_type(h, type));
     TRY(check_mat(h, mat));
-    if (n < 0 || n > INT_MAX) return fail(h, SIGNMUON_E_INVALID, "n must be in [0, 2^31)");
+    if (n < 0 || n > kMaxSize) return fail(h, SIGNMUON_E_INVALID, "n must be in [0, 2^30]");
     if (W == nullptr || !aligned16(W)) return fail(h, SIGNMUON_E_INVALID, "W null or misaligned");
     const sm::MatInfo& mi = h->plan.mats[mat];
+    if (mi.cols > kMaxSize) return fail(h, SIGNMUON_E_UNSUPPORTED, "table rows have at most 2^30 entries");
     TRY(check_ids(h, ids, id_type, n));
     TRY(check_matrix(h, "out", out, type, n, mi.cols, ld));
     NvtxRange range("signmuon embed");
@@ -241,7 +245,7 @@ int signmuon_layernorm(signmuon_t h, const float* W, int gamma, int beta, int64_
     TRY(check_type(h, type));
     int64_t E = 0;
     TRY(norm_mats(h, gamma, beta, &E));
-    if (n < 0 || n > INT_MAX) return fail(h, SIGNMUON_E_INVALID, "n must be in [0, 2^31)");
+    if (n < 0 || n > kMaxSize) return fail(h, SIGNMUON_E_INVALID, "n must be in [0, 2^30]");
     if (W == nullptr || !aligned16(W)) return fail(h, SIGNMUON_E_INVALID, "W null or misaligned");
     if (!(eps > 0.f)) return fail(h, SIGNMUON_E_INVALID, "eps must be > 0");
     TRY(check_matrix(h, "X", X, type, n, E, ldx));

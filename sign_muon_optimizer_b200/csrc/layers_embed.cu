@@ -49,34 +49,66 @@ __global__ void __launch_bounds__(256) k_embed(const float* __restrict__ table, 
 }
 
 // ---------------------------------------------------------------------------
-// Gradient: G[m][v] = scale * sum of dY[r] over worker m's tokens v.
+// Gradient: G[m][v] = scale * sum of dY[r] over worker m's tokens v.  Bound by
+// the bytes: dY read once, M dense tables written once.
 //
 // The tokens of each worker are sorted by (id, row): tiles of kSortTile in
 // shared memory, then 16-way merges by rank (every key is unique, so a key's
 // place in the merge is its own index plus its lower bounds in the other
-// runs).  A warp then takes kEmbTile = 32 sorted tokens of one worker, one key
-// per lane, and adds up their dY rows in registers; a run of equal ids that
-// lies inside the unit is written to G, the parts of a run that crosses units
-// go to the workspace and are added up in order afterwards.  Work per unit
-// does not depend on how often a token occurs.
-// Absent tokens (id < 0, id >= V) get the key UINT_MAX and sort to the end.
+// runs).  The tables are zeroed by further blocks of the same launches, which
+// hides the sort behind those bytes.  A block then takes kEmbUnit = 256 sorted
+// tokens of one worker and a strip of columns, a warp 32 of them, one key per
+// lane, and adds up their dY rows in registers; parts of a run of equal ids are
+// added up in order across the warps through shared memory, and where it goes
+// on in other blocks by k_embed_join.  Work per block does not depend on how
+// often a token occurs, and every sum has a fixed order.
+// Absent tokens (id < 0, id >= V) get the id kAbsent and sort to the end.
 // ---------------------------------------------------------------------------
 typedef unsigned long long Key;  // id in the upper 32 bits, row in the lower
 
 __device__ __forceinline__ unsigned key_id(Key k) { return (unsigned)(k >> 32); }
 constexpr unsigned kAbsent = 0xffffffffu;
 
-// one block per unit of `map` (kSortTile rows of one worker): bitonic sort
-__global__ void __launch_bounds__(1024) k_sort_tiles(const RowMap map, const void* __restrict__ ids, int id64,
-                                                     int64_t V, Key* __restrict__ keys, int* status) {
+// A share of zeroing n floats at G[m] + off, m < M, by `blocks` blocks of 1024
+// threads: block b of them, of share [from, to) in 1/1024ths of each table.
+struct ZeroShare {
+  int64_t off, n;
+  int M, blocks, from, to;
+};
+
+__device__ __forceinline__ void zero_tables(const GradPtrs& G, const ZeroShare& z, int b) {
+  const int per_table = z.blocks / z.M;    // (blocks is a multiple of M)
+  const int m = b / per_table;
+  float* g = G.p[m] + z.off;
+  const int64_t head = min(z.n, (int64_t)((4 - (z.off & 3)) & 3));   // to the first 16-byte boundary
+  const int64_t n4 = (z.n - head) / 4;
+  const int64_t lo = n4 * z.from / 1024, hi = n4 * z.to / 1024;
+  float4* g4 = reinterpret_cast<float4*>(g + head);
+  const int64_t t = (int64_t)(b - m * per_table) * blockDim.x + threadIdx.x, step = (int64_t)per_table * blockDim.x;
+  for (int64_t i = lo + t; i < hi; i += step) g4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (z.from == 0 && t < head) g[t] = 0.f;
+  if (z.to == 1024 && head + 4 * n4 + t < z.n) g[head + 4 * n4 + t] = 0.f;
+}
+
+// a block per unit of `map` (kSortTile rows of one worker): bitonic sort; the
+// blocks behind them zero the tables
+__global__ void __launch_bounds__(1024, 1) k_sort_tiles(const RowMap map, const void* __restrict__ ids, int id64,
+                                                     int64_t V, Key* __restrict__ keys, int* status, const GradPtrs G,
+                                                     const ZeroShare zero) {
   __shared__ Key k[kSortTile];
   griddep_wait();
   griddep_launch();
   const int u = blockIdx.x;
+  if (u >= map.unit[map.M]) {
+    zero_tables(G, zero, u - map.unit[map.M]);
+    return;
+  }
   const int m = worker_of(map.unit, map.M, u);
   const int r0 = map.start[m] + (u - map.unit[m]) * kSortTile;
   const int n = min(kSortTile, map.start[m + 1] - r0);
-  for (int i = threadIdx.x; i < kSortTile; i += 1024) {
+  int top = 2;  // the power of two that is sorted
+  while (top < n) top <<= 1;
+  for (int i = threadIdx.x; i < top; i += 1024) {
     Key key = ~0ull;
     if (i < n) {
       const int64_t id = load_id(ids, id64, r0 + i);
@@ -86,12 +118,13 @@ __global__ void __launch_bounds__(1024) k_sort_tiles(const RowMap map, const voi
     }
     k[i] = key;
   }
-  int top = 2;  // sort no more than the next power of two
-  while (top < n) top <<= 1;
+  __syncthreads();
+  const int i = threadIdx.x;
   for (int size = 2; size <= top; size <<= 1) {
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      __syncthreads();
-      const int i = threadIdx.x;
+      // pairs at strides up to 32 stay within the 64 keys of a warp
+      if (stride >= 32) __syncthreads();
+      else __syncwarp();
       const int lo = 2 * i - (i & (stride - 1));
       if (lo + stride < top) {
         const bool up = (lo & size) == 0;
@@ -104,16 +137,22 @@ __global__ void __launch_bounds__(1024) k_sort_tiles(const RowMap map, const voi
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += 1024) keys[r0 + i] = k[i];
+  for (int j = threadIdx.x; j < n; j += 1024) keys[r0 + j] = k[j];
 }
 
-// one 16-way merge of sorted runs of `run` keys (a thread per key)
-__global__ void __launch_bounds__(256) k_merge(const RowMap map, int64_t run, const Key* __restrict__ src,
-                                               Key* __restrict__ dst) {
+// one 16-way merge of sorted runs of `run` keys (a thread per key); the blocks
+// behind them zero the tables
+__global__ void __launch_bounds__(1024, 1) k_merge(const RowMap map, int64_t run, const Key* __restrict__ src,
+                                                Key* __restrict__ dst, const GradPtrs G, const ZeroShare zero) {
   griddep_wait();
   griddep_launch();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= map.start[map.M]) return;
+  const int n_all = map.start[map.M], mine_blocks = (n_all + 1023) / 1024;
+  if ((int)blockIdx.x >= mine_blocks) {
+    zero_tables(G, zero, blockIdx.x - mine_blocks);
+    return;
+  }
+  const int i = blockIdx.x * 1024 + threadIdx.x;
+  if (i >= n_all) return;
   const int m = worker_of(map.start, map.M, i);
   const int base = map.start[m], n = map.start[m + 1] - base;
   const int at = i - base;
@@ -135,19 +174,11 @@ __global__ void __launch_bounds__(256) k_merge(const RowMap map, int64_t run, co
   dst[base + g0 + rank] = key;
 }
 
-// zero the tables' gradients (before the rows with tokens are written)
-__global__ void __launch_bounds__(256) k_zero_tables(const GradPtrs G, int64_t off, int64_t n) {
+// zero alone (no tokens at all)
+__global__ void __launch_bounds__(1024) k_zero_tables(const GradPtrs G, const ZeroShare zero) {
   griddep_wait();
   griddep_launch();
-  float* g = G.p[blockIdx.y] + off;
-  const int64_t head = min(n, (int64_t)((4 - (off & 3)) & 3));
-  const int64_t t0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  const int64_t n4 = (n - head) / 4;
-  float4* g4 = reinterpret_cast<float4*>(g + head);
-  for (int64_t i = t0; i < n4; i += step) g4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (t0 < head) g[t0] = 0.f;
-  const int64_t tail = head + 4 * n4 + t0;
-  if (tail < n) g[tail] = 0.f;
+  zero_tables(G, zero, blockIdx.x);
 }
 
 template <typename T, bool VEC>
@@ -165,58 +196,93 @@ __device__ __forceinline__ void emit(float* row, int c, int E, int lane, const f
   strip_store_f32<T, VEC>(row, c, E, lane, x);
 }
 
-// a warp per (unit of 32 sorted tokens, strip of columns)
+// a block per (unit of 256 sorted tokens, strip of columns)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
                                                       const T* __restrict__ dY, int64_t ld, int E, int n_strip,
                                                       int64_t off, float scale, int accumulate,
                                                       float* __restrict__ part) {
   constexpr int VL = Elem<T>::V;
+  constexpr int AHEAD = 8;                        // rows loaded before the first is added
+  __shared__ float head[8][VL][32], tail[8][VL][32];  // a warp's part of a run from before, and of one that goes on
+  __shared__ unsigned first_id[9];                // of each warp; [8]: of the unit behind
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int u = (int)(w / n_strip);
-  if (u >= map.unit[map.M]) return;
-  const int c = (int)(w - (int64_t)u * n_strip) * 32 * VL;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int u = blockIdx.x / n_strip;
+  const int c = (blockIdx.x - u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
-  const int i0 = map.start[m] + (u - map.unit[m]) * kEmbTile;
-  const int n = min(kEmbTile, map.start[m + 1] - i0);
+  const int s0 = map.start[m], s1 = map.start[m + 1];
+  const int i0 = s0 + (u - map.unit[m]) * kEmbUnit + w * 32;
+  const int n = max(0, min(32, s1 - i0));
   const Key key = lane < n ? keys[i0 + lane] : ~0ull;
   const unsigned id = key_id(key);
-  if (__shfl_sync(0xffffffffu, id, 0) == kAbsent) return;
-  // the ids beside the unit, to tell whether its first and last run cross it
-  const unsigned before = i0 > map.start[m] ? key_id(keys[i0 - 1]) : kAbsent;
-  const unsigned after = i0 + n < map.start[m + 1] ? key_id(keys[i0 + n]) : kAbsent;
+  const unsigned before = n > 0 && i0 > s0 ? key_id(keys[i0 - 1]) : kAbsent;
+  const unsigned after = n == 32 && i0 + 32 < s1 ? key_id(keys[i0 + 32]) : kAbsent;
+  if (lane == 0) first_id[w] = id;
+  if (w == 7 && lane == 0) first_id[8] = after;
   float* gm = G.p[m] + off;
   float acc[VL];
 #pragma unroll
   for (int j = 0; j < VL; ++j) acc[j] = 0.f;
-  bool head = true;
-  for (int i = 0; i < n; ++i) {
-    const unsigned v = __shfl_sync(0xffffffffu, id, i);
-    if (v == kAbsent) break;
-    const unsigned r = __shfl_sync(0xffffffffu, (unsigned)key, i);
-    float x[VL];
-    strip_load<T, VEC>(dY + (int64_t)r * ld, c, E, lane, x);
+  bool at_head = true;                            // still in the warp's first run
+  unsigned goes_on = kAbsent;                     // the id of the run in tail[w]
+  for (int k = 0; k < n; k += AHEAD) {
+    Pack<T> raw[AHEAD];
 #pragma unroll
-    for (int j = 0; j < VL; ++j) acc[j] += x[j];
-    const unsigned next = i + 1 < n ? __shfl_sync(0xffffffffu, id, i + 1) : after;
-    if (i + 1 < n ? next != v : true) {
-      const bool from_before = head && before == v;
-      const bool goes_on = i + 1 == n && after == v;
-      if (from_before) strip_store_f32<T, VEC>(part + (int64_t)u * 2 * E, c, E, lane, acc);
-      else if (goes_on) strip_store_f32<T, VEC>(part + ((int64_t)u * 2 + 1) * E, c, E, lane, acc);
-      else emit<T, VEC>(gm + (int64_t)v * E, c, E, lane, acc, scale, accumulate);
-      head = false;
-#pragma unroll
-      for (int j = 0; j < VL; ++j) acc[j] = 0.f;
+    for (int a = 0; a < AHEAD; ++a) {
+      const unsigned r = __shfl_sync(0xffffffffu, (unsigned)key, k + a);
+      const bool real = __shfl_sync(0xffffffffu, id, k + a) != kAbsent;
+      raw[a] = strip_raw<T, VEC>(dY + (int64_t)(real ? r : 0) * ld, c, real ? E : 0, lane);
     }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const unsigned v = __shfl_sync(0xffffffffu, id, k + a);
+      if (v == kAbsent) break;
+#pragma unroll
+      for (int j = 0; j < VL; ++j) acc[j] += Elem<T>::up(raw[a].v[j]);
+      const unsigned next = k + a == 31 ? after : __shfl_sync(0xffffffffu, id, (k + a + 1) & 31);
+      const bool last = k + a == 31;
+      if (next != v || last) {
+        if (at_head && before == v) {             // (a run over the whole warp too)
+#pragma unroll
+          for (int j = 0; j < VL; ++j) head[w][j][lane] = acc[j];
+        } else if (next == v) {
+          goes_on = v;
+#pragma unroll
+          for (int j = 0; j < VL; ++j) tail[w][j][lane] = acc[j];
+        } else {
+          emit<T, VEC>(gm + (int64_t)v * E, c, E, lane, acc, scale, accumulate);
+        }
+        at_head = false;
+#pragma unroll
+        for (int j = 0; j < VL; ++j) acc[j] = 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  // runs over several warps: the warp where one starts adds up its parts; the
+  // unit's first warp also those of a run from the unit before
+  const bool from_before = w == 0 && before != kAbsent && before == first_id[0];
+  for (int which = 0; which < 2; ++which) {
+    const bool tail_part = which == 1;
+    if (tail_part ? goes_on == kAbsent : !from_before) continue;
+    const unsigned v = tail_part ? goes_on : before;
+    int j0 = w + 1;                               // the next warp whose head may belong to the run
+#pragma unroll
+    for (int j = 0; j < VL; ++j) acc[j] = tail_part ? tail[w][j][lane] : head[0][j][lane];
+    for (; j0 < 8 && first_id[j0] == v; ++j0)
+#pragma unroll
+      for (int j = 0; j < VL; ++j) acc[j] += head[j0][j][lane];
+    const bool beyond = j0 == 8 && first_id[8] == v;
+    if (!tail_part) strip_store_f32<T, VEC>(part + (int64_t)u * 2 * E, c, E, lane, acc);
+    else if (beyond) strip_store_f32<T, VEC>(part + ((int64_t)u * 2 + 1) * E, c, E, lane, acc);
+    else emit<T, VEC>(gm + (int64_t)v * E, c, E, lane, acc, scale, accumulate);
   }
 }
 
-// a warp per (unit, strip): where a run starts in the unit and goes on, its
-// parts are added up in order and written
+// a warp per (unit, strip): where a run starts in the unit and goes on behind
+// it, its parts are added up in order and written
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
                                                     int E, int n_strip, int64_t off, float scale, int accumulate,
@@ -231,21 +297,26 @@ __global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const Grad
   const int c = (int)(w - (int64_t)u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
   const int s0 = map.start[m], s1 = map.start[m + 1];
-  const int i0 = s0 + (u - map.unit[m]) * kEmbTile;
-  if (i0 + kEmbTile >= s1) return;
-  const unsigned v = key_id(keys[i0 + kEmbTile - 1]);
-  if (v == kAbsent || key_id(keys[i0 + kEmbTile]) != v) return;
+  const int i0 = s0 + (u - map.unit[m]) * kEmbUnit;
+  if (i0 + kEmbUnit >= s1) return;
+  const unsigned v = key_id(keys[i0 + kEmbUnit - 1]);
+  if (v == kAbsent || key_id(keys[i0 + kEmbUnit]) != v) return;
   if (i0 > s0 && key_id(keys[i0]) == v && key_id(keys[i0 - 1]) == v) return;  // the run starts further left
   float acc[VL];
   strip_load_f32<T, VEC>(part + ((int64_t)u * 2 + 1) * E, c, E, lane, acc);
-  int k = u + 1;
-  for (int i = i0 + kEmbTile;; i += kEmbTile, ++k) {
-    float x[VL];
-    strip_load_f32<T, VEC>(part + (int64_t)k * 2 * E, c, E, lane, x);
+  for (int k = u + 1;; k += 32) {
+    // the units behind whose first token belongs to the run, 32 at a time
+    const int64_t at = (int64_t)i0 + (int64_t)(k - u + lane) * kEmbUnit;
+    const unsigned in = __ballot_sync(0xffffffffu, at < s1 && key_id(keys[at < s1 ? at : i0]) == v);
+    const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      float x[VL];
+      strip_load_f32<T, VEC>(part + (int64_t)(k + i) * 2 * E, c, E, lane, x);
 #pragma unroll
-    for (int j = 0; j < VL; ++j) acc[j] += x[j];
-    // on as long as the run fills this unit and enters the next
-    if (i + kEmbTile >= s1 || key_id(keys[i + kEmbTile - 1]) != v || key_id(keys[i + kEmbTile]) != v) break;
+      for (int j = 0; j < VL; ++j) acc[j] += x[j];
+    }
+    if (n < 32) break;
   }
   emit<T, VEC>(G.p[m] + off + (int64_t)v * E, c, E, lane, acc, scale, accumulate);
 }
@@ -261,16 +332,17 @@ void run_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const v
 }
 
 template <typename T, bool VEC>
-void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, const GradPtrs& G, const Key* keys) {
+void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, int64_t longest, const GradPtrs& G,
+                      const Key* keys) {
   const int n_strip = (int)((a.E + 32 * Elem<T>::V - 1) / (32 * Elem<T>::V));
-  const int64_t warps = (int64_t)map.unit[map.M] * n_strip;
-  const unsigned grid = (unsigned)((warps + 7) / 8);
+  const int64_t blocks = (int64_t)map.unit[map.M] * n_strip;
   count_launch();
-  launch_pdl(k_embed_reduce<T, VEC>, dim3(grid), dim3(256), 0, s, map, G, keys, reinterpret_cast<const T*>(a.dY), a.ld,
-             (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part);
+  launch_pdl(k_embed_reduce<T, VEC>, dim3((unsigned)blocks), dim3(256), 0, s, map, G, keys,
+             reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part);
+  if (longest <= kEmbUnit) return;   // no run leaves its unit
   count_launch();
-  launch_pdl(k_embed_join<T, VEC>, dim3(grid), dim3(256), 0, s, map, G, keys, (int)a.E, n_strip, a.off, a.scale,
-             a.accumulate, (const float*)a.part);
+  launch_pdl(k_embed_join<T, VEC>, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, map, G, keys, (int)a.E, n_strip,
+             a.off, a.scale, a.accumulate, (const float*)a.part);
 }
 
 RowMap make_map(const int* start, int M, int tile) {
@@ -300,29 +372,49 @@ void launch_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, cons
 }
 
 void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start, int M, const GradPtrs& G) {
-  if (!a.accumulate) {
-    const int64_t n = a.V * a.E;
-    const int64_t blocks = (n / 4 + 255) / 256 + 1;
-    count_launch();
-    launch_pdl(k_zero_tables, dim3((unsigned)(blocks < 1024 ? blocks : 1024), M), dim3(256), 0, s, G, a.off, n);
-  }
   const int N = start[M];
-  if (N == 0) return;
-  const RowMap sort_map = make_map(start, M, kSortTile);
-  count_launch();
-  launch_pdl(k_sort_tiles, dim3(sort_map.unit[M]), dim3(1024), 0, s, sort_map, a.ids, a.id64, a.V, a.keys[0], a.status);
   int64_t longest = 0;
   for (int m = 0; m < M; ++m) longest = longest > start[m + 1] - start[m] ? longest : start[m + 1] - start[m];
-  int at = 0;
-  for (int64_t run = kSortTile; run < longest; run *= 16, at ^= 1) {
-    count_launch();
-    launch_pdl(k_merge, dim3((unsigned)((N + 255LL) / 256)), dim3(256), 0, s, sort_map, run, (const Key*)a.keys[at],
-               a.keys[at ^ 1]);
+  int merges = 0;
+  for (int64_t run = kSortTile; run < longest; run *= 16) ++merges;
+  // the tables are zeroed in equal shares beside the sort and each merge:
+  // eight blocks to an SM, so that they even out, but at least 16 KB a block
+  ZeroShare z{};
+  z.off = a.off;
+  z.n = a.V * a.E;
+  z.M = M;
+  z.to = 1024;
+  if (!a.accumulate) {
+    const int64_t want = (8 * num_sms() + M - 1) / M, most = (z.n + 4095) / 4096;
+    z.blocks = M * (int)(want < most ? want : most);
   }
-  const RowMap map = make_map(start, M, kEmbTile);
+  if (N == 0) {
+    if (z.blocks > 0) {
+      count_launch();
+      launch_pdl(k_zero_tables, dim3(z.blocks), dim3(1024), 0, s, G, z);
+    }
+    return;
+  }
+  const RowMap sort_map = make_map(start, M, kSortTile);
+  z.to = 1024 / (merges + 1);
+  count_launch();
+  launch_pdl(k_sort_tiles, dim3(sort_map.unit[M] + z.blocks), dim3(1024), 0, s, sort_map, a.ids, a.id64, a.V, a.keys[0],
+             a.status, G, z);
+  int at = 0;
+  int64_t run = kSortTile;
+  for (int i = 1; i <= merges; ++i, run *= 16, at ^= 1) {
+    z.from = z.to;
+    z.to = i == merges ? 1024 : 1024 * (i + 1) / (merges + 1);
+    count_launch();
+    launch_pdl(k_merge, dim3((unsigned)((N + 1023LL) / 1024) + z.blocks), dim3(1024), 0, s, sort_map, run,
+               (const Key*)a.keys[at], a.keys[at ^ 1], G, z);
+  }
+  const RowMap map = make_map(start, M, kEmbUnit);
   const int vl = a.type == LT_F32 ? 4 : 8;
-  bool vec = a.E % vl == 0 && a.ld % vl == 0 && a.off % 4 == 0 && on16(a.dY);
-#define SM_RUN(T) (vec ? run_embed_reduce<T, true>(s, a, map, G, a.keys[at]) : run_embed_reduce<T, false>(s, a, map, G, a.keys[at]))
+  const bool vec = a.E % vl == 0 && a.ld % vl == 0 && a.off % 4 == 0 && on16(a.dY);
+#define SM_RUN(T)                                                             \
+  (vec ? run_embed_reduce<T, true>(s, a, map, longest, G, a.keys[at])         \
+       : run_embed_reduce<T, false>(s, a, map, longest, G, a.keys[at]))
   if (a.type == LT_F32) SM_RUN(float);
   else if (a.type == LT_BF16) SM_RUN(__nv_bfloat16);
   else SM_RUN(__half);

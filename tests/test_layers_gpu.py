@@ -93,6 +93,11 @@ def ids_of(kind, n, V, g):
         return ((V + 1.0) ** torch.rand(n, generator=g, device="cuda", dtype=torch.float64)).long().clamp(1, V) - 1
     if kind == "same":
         return torch.full((n,), V // 2, device="cuda")
+    if kind == "lengths":            # runs that end before, at and behind every border of 32 and 256 tokens
+        c = torch.tensor([1, 31, 32, 33, 64, 1, 95, 255, 256, 257, 2, 512, 30, 770], device="cuda")
+        ids = torch.repeat_interleave(torch.arange(len(c), device="cuda"), c)
+        ids = ids.repeat(n // len(ids) + 1)[:n]
+        return ids[torch.randperm(n, generator=g, device="cuda")]
     if kind == "absent":
         return torch.full((n,), -1, device="cuda")
     return torch.arange(n, device="cuda").flip(0) % V   # "falling"
@@ -114,6 +119,11 @@ def ids_of(kind, n, V, g):
     ("f32", [40000, 5, 2048], 700, 4, "zipf", 0, False),     # 20 sorted tiles: two merges
     ("f32", [33000], 20000, 8, "random", 0, False),
     ("bf16", [4096, 4097], 3, 16, "same", 0, False),         # one run over many units
+    ("f32", [12000], 20, 16, "same", 0, False),              # ... over more than 32
+    ("bf16", [2339, 2340, 2338], 14, 40, "lengths", 0, False),
+    ("f32", [4678], 20, 3, "lengths", 0, False),
+    ("f16", [256, 512, 255, 257], 2, 300, "random", 0, False),
+    ("f32", [1, 2] * 128, 9, 5, "random", 0, False),         # 256 workers
 ])
 def test_embed_grad(dt, rows, V, E, kind, gap, accumulate):
     n, M = sum(rows), len(rows)
