@@ -248,8 +248,13 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) 
 #endif  // __CUDACC__
 
 // ---- launch wrappers (host) ------------------------------------------------
-constexpr int kEmbUnit = 256;    // sorted tokens of one block of the reduction
-constexpr int kSortTile = 2048;  // tokens sorted by one block
+constexpr int kSortTile = 2048;   // tokens of a worker that one block sorts
+constexpr int kRadixTile = 2048;  // ... and that a block of the radix sort takes
+constexpr int kRadixBins = 512, kRadixSets = 4;
+// sorted tokens that a warp of the table gradient's reduction takes (a unit is
+// eight warps'): few tokens are spread over more blocks
+constexpr int64_t kFewRows = 32768;
+inline int embed_per_warp(int64_t rows) { return rows <= kFewRows ? 8 : 32; }
 
 void launch_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const void* ids, int id64, int64_t n,
                   float scale, void* out, int type, int64_t ld, int* status);
@@ -264,7 +269,9 @@ struct EmbedGradArgs {
   int64_t off;                 // the table's place in G[m]
   int accumulate;
   unsigned long long* keys[2]; // workspace: one (id, row) key per row, twice
-  float* part;                 // workspace: 2 x E floats per unit of kEmbUnit tokens
+  int* counts;                 // workspace: kRadixSets sets of kRadixBins counts per radix tile
+  int64_t count_set;           // ints in a set
+  float* part;                 // workspace: 2 x E floats per unit of 8 * embed_per_warp tokens
   int* status;
 };
 void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start, int M, const GradPtrs& G);

@@ -108,11 +108,15 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // worker, whose last unit may be short
 int norm_blocks(signmuon_t h) { return h->n_sm * 8 + h->M; }
 
-// workspace layout, in bytes: embed_grad has two key arrays and the parts of
-// cut runs, layernorm_grad the blocks' sums, distill the rows' losses
-int64_t embed_units(signmuon_t h, int64_t rows) { return rows / sm::kEmbUnit + h->M + 1; }
+// workspace layout, in bytes: embed_grad has two key arrays, digit counts and
+// the parts of cut runs, layernorm_grad the blocks' sums, distill the rows' losses
+int64_t embed_units(signmuon_t h, int64_t rows) {
+  const int64_t few = rows < sm::kFewRows ? rows : sm::kFewRows, a = few / 64, b = rows / 256;   // (8 * embed_per_warp)
+  return (a > b ? a : b) + h->M + 1;
+}
+int64_t count_set(signmuon_t h, int64_t rows) { return (rows / sm::kRadixTile + h->M + 1) * sm::kRadixBins; }
 int64_t embed_bytes(signmuon_t h, int64_t rows, int64_t cols) {
-  return 2 * align256(rows * 8) + embed_units(h, rows) * 2 * cols * 4;
+  return 2 * align256(rows * 8) + sm::kRadixSets * count_set(h, rows) * 4 + embed_units(h, rows) * 2 * cols * 4;
 }
 int64_t norm_bytes(signmuon_t h, int64_t cols) {
   return cols <= SIGNMUON_LAYERNORM_MAX_COLS ? (int64_t)norm_blocks(h) * 2 * cols * 4 : 0;
@@ -215,7 +219,9 @@ int signmuon_embed_grad(signmuon_t h, int mat, const void* ids, int id_type, con
     a.accumulate = accumulate != 0;
     a.keys[0] = reinterpret_cast<unsigned long long*>(h->lay_ws);
     a.keys[1] = reinterpret_cast<unsigned long long*>(h->lay_ws + align256(h->lay_rows * 8));
-    a.part = reinterpret_cast<float*>(h->lay_ws + 2 * align256(h->lay_rows * 8));
+    a.counts = reinterpret_cast<int*>(h->lay_ws + 2 * align256(h->lay_rows * 8));
+    a.count_set = count_set(h, h->lay_rows);
+    a.part = reinterpret_cast<float*>(a.counts + sm::kRadixSets * a.count_set);
     a.status = h->lay_status;
     NvtxRange range("signmuon embed_grad");
     sm::launch_embed_grad(h->stream, a, start, h->M, gp);

@@ -52,133 +52,282 @@ __global__ void __launch_bounds__(256) k_embed(const float* __restrict__ table, 
 // Gradient: G[m][v] = scale * sum of dY[r] over worker m's tokens v.  Bound by
 // the bytes: dY read once, M dense tables written once.
 //
-// The tokens of each worker are sorted by (id, row): tiles of kSortTile in
-// shared memory, then 16-way merges by rank (every key is unique, so a key's
-// place in the merge is its own index plus its lower bounds in the other
-// runs).  The tables are zeroed by further blocks of the same launches, which
-// hides the sort behind those bytes.  A block then takes kEmbUnit = 256 sorted
-// tokens of one worker and a strip of columns, a warp 32 of them, one key per
-// lane, and adds up their dY rows in registers; parts of a run of equal ids are
-// added up in order across the warps through shared memory, and where it goes
-// on in other blocks by k_embed_join.  Work per block does not depend on how
-// often a token occurs, and every sum has a fixed order.
+// The tokens of each worker are sorted by (id, row): up to kSortTile of them in
+// registers, more by a radix sort.  A block then takes a unit of sorted tokens of one worker and a strip
+// of columns, a warp an eighth of them, one key per lane, and adds up their dY
+// rows in registers; parts of a run of equal ids are added up in order across
+// the warps through shared memory, and where it goes on in other blocks by
+// k_embed_join.  Work per block does not depend on how often a token occurs,
+// and every sum has a fixed order.  Further blocks of the same launch write
+// zeros to the rows without tokens, so that every byte of G is written once.
 // Absent tokens (id < 0, id >= V) get the id kAbsent and sort to the end.
 // ---------------------------------------------------------------------------
 typedef unsigned long long Key;  // id in the upper 32 bits, row in the lower
 
 __device__ __forceinline__ unsigned key_id(Key k) { return (unsigned)(k >> 32); }
 constexpr unsigned kAbsent = 0xffffffffu;
+constexpr int kSortThreads = 512;
 
-// A share of zeroing n floats at G[m] + off, m < M, by `blocks` blocks of 1024
-// threads: block b of them, of share [from, to) in 1/1024ths of each table.
-struct ZeroShare {
-  int64_t off, n;
-  int M, blocks, from, to;
-};
-
-__device__ __forceinline__ void zero_tables(const GradPtrs& G, const ZeroShare& z, int b) {
-  const int per_table = z.blocks / z.M;    // (blocks is a multiple of M)
-  const int m = b / per_table;
-  float* g = G.p[m] + z.off;
-  const int64_t head = min(z.n, (int64_t)((4 - (z.off & 3)) & 3));   // to the first 16-byte boundary
-  const int64_t n4 = (z.n - head) / 4;
-  const int64_t lo = n4 * z.from / 1024, hi = n4 * z.to / 1024;
-  float4* g4 = reinterpret_cast<float4*>(g + head);
-  const int64_t t = (int64_t)(b - m * per_table) * blockDim.x + threadIdx.x, step = (int64_t)per_table * blockDim.x;
-  for (int64_t i = lo + t; i < hi; i += step) g4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (z.from == 0 && t < head) g[t] = 0.f;
-  if (z.to == 1024 && head + 4 * n4 + t < z.n) g[head + 4 * n4 + t] = 0.f;
+template <typename K>
+__device__ __forceinline__ K shfl_xor(K v, int lanes) {
+  return __shfl_xor_sync(0xffffffffu, v, lanes);
 }
 
-// a block per unit of `map` (kSortTile rows of one worker): bitonic sort; the
-// blocks behind them zero the tables
-__global__ void __launch_bounds__(1024, 1) k_sort_tiles(const RowMap map, const void* __restrict__ ids, int id64,
-                                                     int64_t V, Key* __restrict__ keys, int* status, const GradPtrs G,
-                                                     const ZeroShare zero) {
-  __shared__ Key k[kSortTile];
+// a block per unit of `map` (kSortTile rows of one worker): bitonic sort, PER
+// keys a thread, with exchanges in registers within a thread, by shuffles
+// within a warp and through shared memory beyond.  K = unsigned: the key is
+// (id, place in the tile) in 32 bits (V below 2^(32 - kPlaceBits)); else 64.
+constexpr int kPlaceBits = 11;
+static_assert(kSortTile == 1 << kPlaceBits, "a place in the tile has kPlaceBits bits");
+template <typename K>
+__global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, const void* __restrict__ ids, int id64,
+                                                             int64_t V, Key* __restrict__ keys, int* status) {
+  constexpr int THREADS = kSortThreads;
+  constexpr int PER = kSortTile / THREADS;
+  __shared__ K swap[kSortTile];
   griddep_wait();
   griddep_launch();
   const int u = blockIdx.x;
-  if (u >= map.unit[map.M]) {
-    zero_tables(G, zero, u - map.unit[map.M]);
-    return;
-  }
   const int m = worker_of(map.unit, map.M, u);
   const int r0 = map.start[m] + (u - map.unit[m]) * kSortTile;
   const int n = min(kSortTile, map.start[m + 1] - r0);
-  int top = 2;  // the power of two that is sorted
-  while (top < n) top <<= 1;
-  for (int i = threadIdx.x; i < top; i += 1024) {
-    Key key = ~0ull;
+  const int tid = threadIdx.x;
+  constexpr K kNone = (K)~(K)0;                   // absent tokens and places beyond n
+  K k[PER];                                       // the keys of places tid * PER ... + PER - 1
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * THREADS + tid;
+    K key = kNone;
     if (i < n) {
       const int64_t id = load_id(ids, id64, r0 + i);
       if (id >= V) *status = 1;
-      const unsigned w = (id >= 0 && id < V) ? (unsigned)id : kAbsent;
-      key = ((Key)w << 32) | (unsigned)(r0 + i);
+      const K w = (id >= 0 && id < V) ? (K)id : (K)(kNone >> kPlaceBits);
+      key = (K)(w << kPlaceBits) | (K)i;
     }
-    k[i] = key;
+    swap[i] = key;
   }
   __syncthreads();
-  const int i = threadIdx.x;
-  for (int size = 2; size <= top; size <<= 1) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) k[j] = swap[tid * PER + j];
+  for (int size = 2; size < n * 2; size <<= 1) {
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      // pairs at strides up to 32 stay within the 64 keys of a warp
-      if (stride >= 32) __syncthreads();
-      else __syncwarp();
-      const int lo = 2 * i - (i & (stride - 1));
-      if (lo + stride < top) {
-        const bool up = (lo & size) == 0;
-        const Key a = k[lo], b = k[lo + stride];
-        if ((a > b) == up) {
-          k[lo] = b;
-          k[lo + stride] = a;
+      if (stride >= PER) {
+        K other[PER];
+        if (stride < 32 * PER) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) other[j] = shfl_xor(k[j], stride / PER);
+        } else {
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < PER; ++j) swap[j * THREADS + tid] = k[j];
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < PER; ++j) other[j] = swap[j * THREADS + (tid ^ (stride / PER))];
+        }
+        const bool keep_min = ((tid * PER & stride) == 0) == ((tid * PER & size) == 0);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) k[j] = (k[j] < other[j]) == keep_min ? k[j] : other[j];
+      } else {
+#pragma unroll
+        for (int d = PER / 2; d > 0; d >>= 1) {
+          if (d != stride) continue;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) {
+            if (j & d) continue;
+            const K a = k[j], b = k[j | d];
+            const bool swapped = (a > b) == (((tid * PER + j) & size) == 0);
+            k[j] = swapped ? b : a;
+            k[j | d] = swapped ? a : b;
+          }
         }
       }
     }
   }
   __syncthreads();
-  for (int j = threadIdx.x; j < n; j += 1024) keys[r0 + j] = k[j];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) swap[tid * PER + j] = k[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * THREADS + tid;
+    if (i >= n) continue;
+    const K w = swap[i] >> kPlaceBits;
+    const unsigned id = w == (K)(kNone >> kPlaceBits) ? kAbsent : (unsigned)w;
+    keys[r0 + i] = ((Key)id << 32) | (unsigned)(r0 + (int)(swap[i] & (K)(kSortTile - 1)));
+  }
 }
 
-// one 16-way merge of sorted runs of `run` keys (a thread per key); the blocks
-// behind them zero the tables
-__global__ void __launch_bounds__(1024, 1) k_merge(const RowMap map, int64_t run, const Key* __restrict__ src,
-                                                Key* __restrict__ dst, const GradPtrs G, const ZeroShare zero) {
+// Radix sort of longer token lists, least significant digit first, kRadixTile
+// tokens of one worker a block.  Within a worker digit d of tile u starts at
+// (tokens with a smaller digit) + (tokens with d in the tiles before u), from the
+// tiles' digit counts; a token's place behind that comes from counting in order:
+// warps take 32 tokens at a time and match equal digits.
+// The first counts are made by k_radix_count; each scatter makes the next
+// digit's by (integer) atomics.  There is a set of counts per digit.  Absent tokens sort as id V.
+constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
+static_assert(kBins == kRadixBins && kRadixSets * kDigitBits >= 31, "the workspace has a set of counts per digit");
+
+__device__ __forceinline__ unsigned radix_id(const void* ids, int id64, int64_t V, int i) {
+  const int64_t id = load_id(ids, id64, i);
+  return (unsigned)(id >= 0 && id < V ? id : V);
+}
+
+__global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const void* __restrict__ ids, int id64, int64_t V,
+                                                     int bits, int digits, int* __restrict__ count, int64_t set,
+                                                     int* status) {
+  __shared__ int c[kBins];
   griddep_wait();
   griddep_launch();
-  const int n_all = map.start[map.M], mine_blocks = (n_all + 1023) / 1024;
-  if ((int)blockIdx.x >= mine_blocks) {
-    zero_tables(G, zero, blockIdx.x - mine_blocks);
-    return;
+  const int u = blockIdx.x;
+  const int m = worker_of(map.unit, map.M, u);
+  const int r0 = map.start[m] + (u - map.unit[m]) * kRadixTile;
+  const int n = min(kRadixTile, map.start[m + 1] - r0);
+  for (int d = threadIdx.x; d < kBins; d += 256) {
+    c[d] = 0;
+    for (int k = 1; k < digits; ++k) count[k * set + (int64_t)u * kBins + d] = 0;
   }
-  const int i = blockIdx.x * 1024 + threadIdx.x;
-  if (i >= n_all) return;
-  const int m = worker_of(map.start, map.M, i);
-  const int base = map.start[m], n = map.start[m + 1] - base;
-  const int at = i - base;
-  const int64_t g0 = at / (16 * run) * (16 * run);
-  const int64_t mine = at / run;
-  const Key key = src[i];
-  int64_t rank = at - mine * run;
-  for (int64_t q = g0; q < g0 + 16 * run && q < n; q += run) {
-    if (q == mine * run) continue;
-    const Key* p = src + base + q;
-    int lo = 0, hi = (int)(run < n - q ? run : n - q);  // keys of the run below `key`
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += 256) {
+    if (load_id(ids, id64, r0 + i) >= V) *status = 1;
+    atomicAdd(&c[radix_id(ids, id64, V, r0 + i) & ((1u << bits) - 1)], 1);
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < kBins; d += 256) count[(int64_t)u * kBins + d] = c[d];
+}
+
+// src = null: the first digit, keys from the ids; next = null: the last digit
+__global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const void* __restrict__ ids, int id64,
+                                                       int64_t V, int shift, int bits, const Key* __restrict__ src,
+                                                       Key* __restrict__ dst, int* __restrict__ count,
+                                                       int* __restrict__ next) {
+  constexpr int ROUNDS = kRadixTile / 256;
+  __shared__ int warp_count[8][kBins];
+  __shared__ int base[kBins];
+  __shared__ int scan[8];
+  griddep_wait();
+  griddep_launch();
+  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int m = worker_of(map.unit, map.M, u);
+  const int r0 = map.start[m] + (u - map.unit[m]) * kRadixTile;
+  const int n = min(kRadixTile, map.start[m + 1] - r0);
+  const unsigned mask = (1u << bits) - 1;
+  Key key[ROUNDS];
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {   // warp w has tokens w * 32 * ROUNDS on, 32 of them a round
+    const int i = (w * ROUNDS + j) * 32 + lane;
+    key[j] = ~0ull;
+    if (i < n) {
+      if (src != nullptr) key[j] = src[r0 + i];
+      else key[j] = ((Key)radix_id(ids, id64, V, r0 + i) << 32) | (unsigned)(r0 + i);
+    }
+  }
+  for (int d = tid; d < 8 * kBins; d += 256) (&warp_count[0][0])[d] = 0;
+  // where each digit of this tile starts: two neighbouring digits a thread
+  const int u0 = map.unit[m], u1 = map.unit[m + 1];
+  int all0 = 0, all1 = 0, before0 = 0, before1 = 0;
+#pragma unroll 4
+  for (int k = u0; k < u1; ++k) {
+    const int2 c = *reinterpret_cast<const int2*>(count + (int64_t)k * kBins + 2 * tid);
+    all0 += c.x;
+    all1 += c.y;
+    if (k < u) {
+      before0 += c.x;
+      before1 += c.y;
+    }
+  }
+  int sum = all0 + all1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += t;
+  }
+  if (lane == 31) scan[w] = sum;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) sum += scan[i];
+  base[2 * tid] = sum - all0 - all1 + before0;
+  base[2 * tid + 1] = sum - all1 + before1;
+  // counts of the warp so far, and each token's place among its digit's
+  int place[ROUNDS];
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {
+    const bool live = (w * ROUNDS + j) * 32 + lane < n;
+    const unsigned d = live ? (key_id(key[j]) >> shift) & mask : (unsigned)kBins;
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int lower = __popc(same & ((1u << lane) - 1));
+    place[j] = live ? warp_count[w][d] + lower : 0;
+    __syncwarp();
+    if (live && lower == 0) warp_count[w][d] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int d = tid; d < kBins; d += 256) {
+    int run = base[d];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = warp_count[i][d];
+      warp_count[i][d] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {
+    if ((w * ROUNDS + j) * 32 + lane >= n) continue;
+    const unsigned id = key_id(key[j]);
+    const int at = warp_count[w][(id >> shift) & mask] + place[j];
+    if (next != nullptr) {
+      dst[map.start[m] + at] = key[j];
+      atomicAdd(&next[(int64_t)(u0 + at / kRadixTile) * kBins + ((id >> (shift + bits)) & mask)], 1);
+    } else {
+      dst[map.start[m] + at] = id == (unsigned)V ? (key[j] | ((Key)kAbsent << 32)) : key[j];
+    }
+  }
+}
+
+// Zeros for the rows without tokens: group b of `rows` table rows.  A thread
+// per row looks for its id in the worker's sorted keys; then L lanes write a row.
+struct ZeroRows {
+  int M, groups;       // groups per table
+  int rows, L;
+  int64_t off, V;
+};
+
+__device__ __forceinline__ void zero_rows(const RowMap& map, const GradPtrs& G, const Key* __restrict__ keys, int E,
+                                          const ZeroRows& z, int b, unsigned char* empty) {
+  const int m = b / z.groups;
+  const int64_t v0 = (int64_t)(b - m * z.groups) * z.rows;
+  const int t = threadIdx.x;
+  if (t < z.rows && v0 + t < z.V) {
+    const Key want = (Key)(v0 + t) << 32;
+    int lo = map.start[m], hi = map.start[m + 1];
+    const int end = hi;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p[mid] < key) lo = mid + 1;
+      const int mid = lo + ((hi - lo) >> 1);
+      if (keys[mid] < want) lo = mid + 1;
       else hi = mid;
     }
-    rank += lo;
+    empty[t] = !(lo < end && key_id(keys[lo]) == (unsigned)(v0 + t));
   }
-  dst[base + g0 + rank] = key;
+  __syncthreads();
+  const int per = 256 / z.L, l = t % z.L;
+  for (int r = t / z.L; r < z.rows && v0 + r < z.V; r += per) {
+    if (!empty[r]) continue;
+    float* g = G.p[m] + z.off + (v0 + r) * E;
+    const int head = min(E, (int)((4 - (reinterpret_cast<uintptr_t>(g) >> 2 & 3)) & 3));
+    const int n4 = (E - head) / 4;
+    if (l < head) g[l] = 0.f;
+    for (int i = l; i < n4; i += z.L) reinterpret_cast<float4*>(g + head)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = head + 4 * n4 + l; i < E; i += z.L) g[i] = 0.f;
+    for (int i = l + z.L; i < head; i += z.L) g[i] = 0.f;
+  }
 }
 
-// zero alone (no tokens at all)
-__global__ void __launch_bounds__(1024) k_zero_tables(const GradPtrs G, const ZeroShare zero) {
+// zeros alone (no tokens at all)
+__global__ void __launch_bounds__(256) k_zero_rows(const RowMap map, const GradPtrs G, int E, const ZeroRows zero) {
+  __shared__ unsigned char empty[256];
   griddep_wait();
   griddep_launch();
-  zero_tables(G, zero, blockIdx.x);
+  zero_rows(map, G, nullptr, E, zero, blockIdx.x, empty);
 }
 
 template <typename T, bool VEC>
@@ -196,29 +345,36 @@ __device__ __forceinline__ void emit(float* row, int c, int E, int lane, const f
   strip_store_f32<T, VEC>(row, c, E, lane, x);
 }
 
-// a block per (unit of 256 sorted tokens, strip of columns)
+// a block per (unit of 8 * per_warp sorted tokens, strip of columns); the
+// blocks behind them zero the rows without tokens
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
                                                       const T* __restrict__ dY, int64_t ld, int E, int n_strip,
                                                       int64_t off, float scale, int accumulate,
-                                                      float* __restrict__ part) {
+                                                      float* __restrict__ part, int per_warp, const ZeroRows zero) {
   constexpr int VL = Elem<T>::V;
-  constexpr int AHEAD = 8;                        // rows loaded before the first is added
+  constexpr int AHEAD = VEC ? 4 : 8;              // rows in a batch
+  constexpr int BATCHES = 3;                      // VEC: batches on their way
+  extern __shared__ uint4 ring[];                 // VEC: [8 warps][BATCHES * AHEAD][32 lanes]
   __shared__ float head[8][VL][32], tail[8][VL][32];  // a warp's part of a run from before, and of one that goes on
   __shared__ unsigned first_id[9];                // of each warp; [8]: of the unit behind
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int u = blockIdx.x / n_strip;
+  if (u >= map.unit[map.M]) {
+    zero_rows(map, G, keys, E, zero, blockIdx.x - map.unit[map.M] * n_strip, reinterpret_cast<unsigned char*>(head));
+    return;
+  }
   const int c = (blockIdx.x - u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
   const int s0 = map.start[m], s1 = map.start[m + 1];
-  const int i0 = s0 + (u - map.unit[m]) * kEmbUnit + w * 32;
-  const int n = max(0, min(32, s1 - i0));
+  const int i0 = s0 + ((u - map.unit[m]) * 8 + w) * per_warp;
+  const int n = max(0, min(per_warp, s1 - i0));
   const Key key = lane < n ? keys[i0 + lane] : ~0ull;
   const unsigned id = key_id(key);
   const unsigned before = n > 0 && i0 > s0 ? key_id(keys[i0 - 1]) : kAbsent;
-  const unsigned after = n == 32 && i0 + 32 < s1 ? key_id(keys[i0 + 32]) : kAbsent;
+  const unsigned after = n == per_warp && i0 + n < s1 ? key_id(keys[i0 + n]) : kAbsent;
   if (lane == 0) first_id[w] = id;
   if (w == 7 && lane == 0) first_id[8] = after;
   float* gm = G.p[m] + off;
@@ -227,22 +383,45 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
   for (int j = 0; j < VL; ++j) acc[j] = 0.f;
   bool at_head = true;                            // still in the warp's first run
   unsigned goes_on = kAbsent;                     // the id of the run in tail[w]
-  for (int k = 0; k < n; k += AHEAD) {
-    Pack<T> raw[AHEAD];
+  // the absent tokens are the last ones
+  const int real = __popc(__ballot_sync(0xffffffffu, id != kAbsent));
+  uint4* slots = &ring[w * (BATCHES * AHEAD * 32) + lane];
+  auto fetch = [&](int k, int batch) {            // the rows from token k on
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
-      const unsigned r = __shfl_sync(0xffffffffu, (unsigned)key, k + a);
-      const bool real = __shfl_sync(0xffffffffu, id, k + a) != kAbsent;
-      raw[a] = strip_raw<T, VEC>(dY + (int64_t)(real ? r : 0) * ld, c, real ? E : 0, lane);
+      const unsigned r = __shfl_sync(0xffffffffu, (unsigned)key, (k + a) & 31);
+      const int col = c + lane * VL;
+      if (k + a < real && col < E) copy16(slots + (batch * AHEAD + a) * 32, dY + (int64_t)r * ld + col, true);
     }
+    copy_commit();
+  };
+  if (VEC) {
+#pragma unroll
+    for (int b = 0; b < BATCHES; ++b) fetch(b * AHEAD, b);
+  }
+  int batch = 0;
+  for (int k = 0; k < real; k += AHEAD) {
+    Pack<T> raw[AHEAD];
+    if (VEC) copy_wait<BATCHES - 1>();
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
+      if (VEC) {
+        raw[a] = *reinterpret_cast<const Pack<T>*>(slots + (batch * AHEAD + a) * 32);
+      } else {
+        const unsigned r = __shfl_sync(0xffffffffu, (unsigned)key, k + a);
+        raw[a] = strip_raw<T, VEC>(dY + (int64_t)(k + a < real ? r : 0) * ld, c, k + a < real ? E : 0, lane);
+      }
+    }
+    if (VEC) fetch(k + BATCHES * AHEAD, batch);
+    batch = batch + 1 == BATCHES ? 0 : batch + 1;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      if (k + a >= real) break;
       const unsigned v = __shfl_sync(0xffffffffu, id, k + a);
-      if (v == kAbsent) break;
 #pragma unroll
       for (int j = 0; j < VL; ++j) acc[j] += Elem<T>::up(raw[a].v[j]);
-      const unsigned next = k + a == 31 ? after : __shfl_sync(0xffffffffu, id, (k + a + 1) & 31);
-      const bool last = k + a == 31;
+      const bool last = k + a == per_warp - 1;
+      const unsigned next = last ? after : __shfl_sync(0xffffffffu, id, (k + a + 1) & 31);
       if (next != v || last) {
         if (at_head && before == v) {             // (a run over the whole warp too)
 #pragma unroll
@@ -286,7 +465,7 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
                                                     int E, int n_strip, int64_t off, float scale, int accumulate,
-                                                    const float* __restrict__ part) {
+                                                    const float* __restrict__ part, int unit) {
   constexpr int VL = Elem<T>::V;
   griddep_wait();
   griddep_launch();
@@ -297,16 +476,16 @@ __global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const Grad
   const int c = (int)(w - (int64_t)u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
   const int s0 = map.start[m], s1 = map.start[m + 1];
-  const int i0 = s0 + (u - map.unit[m]) * kEmbUnit;
-  if (i0 + kEmbUnit >= s1) return;
-  const unsigned v = key_id(keys[i0 + kEmbUnit - 1]);
-  if (v == kAbsent || key_id(keys[i0 + kEmbUnit]) != v) return;
+  const int i0 = s0 + (u - map.unit[m]) * unit;
+  if (i0 + unit >= s1) return;
+  const unsigned v = key_id(keys[i0 + unit - 1]);
+  if (v == kAbsent || key_id(keys[i0 + unit]) != v) return;
   if (i0 > s0 && key_id(keys[i0]) == v && key_id(keys[i0 - 1]) == v) return;  // the run starts further left
   float acc[VL];
   strip_load_f32<T, VEC>(part + ((int64_t)u * 2 + 1) * E, c, E, lane, acc);
   for (int k = u + 1;; k += 32) {
     // the units behind whose first token belongs to the run, 32 at a time
-    const int64_t at = (int64_t)i0 + (int64_t)(k - u + lane) * kEmbUnit;
+    const int64_t at = (int64_t)i0 + (int64_t)(k - u + lane) * unit;
     const unsigned in = __ballot_sync(0xffffffffu, at < s1 && key_id(keys[at < s1 ? at : i0]) == v);
     const int n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
 #pragma unroll 4
@@ -332,17 +511,21 @@ void run_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const v
 }
 
 template <typename T, bool VEC>
-void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, int64_t longest, const GradPtrs& G,
-                      const Key* keys) {
+void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, int per_warp, int64_t longest,
+                      const GradPtrs& G, const Key* keys, const ZeroRows& zero) {
   const int n_strip = (int)((a.E + 32 * Elem<T>::V - 1) / (32 * Elem<T>::V));
   const int64_t blocks = (int64_t)map.unit[map.M] * n_strip;
+  auto* reduce = k_embed_reduce<T, VEC>;
+  const size_t smem = VEC ? 8 * 3 * 4 * 32 * 16 : 0;
+  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)reduce, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   count_launch();
-  launch_pdl(k_embed_reduce<T, VEC>, dim3((unsigned)blocks), dim3(256), 0, s, map, G, keys,
-             reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part);
-  if (longest <= kEmbUnit) return;   // no run leaves its unit
+  launch_pdl(reduce, dim3((unsigned)(blocks + (int64_t)zero.M * zero.groups)), dim3(256), smem, s, map, G, keys,
+             reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part, per_warp,
+             zero);
+  if (longest <= 8 * per_warp) return;   // no run leaves its unit
   count_launch();
   launch_pdl(k_embed_join<T, VEC>, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, map, G, keys, (int)a.E, n_strip,
-             a.off, a.scale, a.accumulate, (const float*)a.part);
+             a.off, a.scale, a.accumulate, (const float*)a.part, 8 * per_warp);
 }
 
 RowMap make_map(const int* start, int M, int tile) {
@@ -375,46 +558,55 @@ void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start,
   const int N = start[M];
   int64_t longest = 0;
   for (int m = 0; m < M; ++m) longest = longest > start[m + 1] - start[m] ? longest : start[m + 1] - start[m];
-  int merges = 0;
-  for (int64_t run = kSortTile; run < longest; run *= 16) ++merges;
-  // the tables are zeroed in equal shares beside the sort and each merge:
-  // eight blocks to an SM, so that they even out, but at least 16 KB a block
-  ZeroShare z{};
-  z.off = a.off;
-  z.n = a.V * a.E;
-  z.M = M;
-  z.to = 1024;
+  ZeroRows z{};
   if (!a.accumulate) {
-    const int64_t want = (8 * num_sms() + M - 1) / M, most = (z.n + 4095) / 4096;
-    z.blocks = M * (int)(want < most ? want : most);
+    // about 128 KB of table rows a block, at most one row per thread
+    const int64_t fit = 32768 / a.E;
+    z.M = M;
+    z.rows = (int)(fit < 1 ? 1 : fit > 256 ? 256 : fit);
+    z.groups = (int)((a.V + z.rows - 1) / z.rows);
+    z.L = 1;
+    while (z.L < 32 * (z.rows < 8 ? 8 : 1) && z.L * 4 < a.E) z.L <<= 1;
+    z.off = a.off;
+    z.V = a.V;
   }
   if (N == 0) {
-    if (z.blocks > 0) {
-      count_launch();
-      launch_pdl(k_zero_tables, dim3(z.blocks), dim3(1024), 0, s, G, z);
-    }
+    if (z.M == 0) return;
+    const RowMap none = make_map(start, M, kSortTile);
+    count_launch();
+    launch_pdl(k_zero_rows, dim3((unsigned)((int64_t)M * z.groups)), dim3(256), 0, s, none, G, (int)a.E, z);
     return;
   }
-  const RowMap sort_map = make_map(start, M, kSortTile);
-  z.to = 1024 / (merges + 1);
-  count_launch();
-  launch_pdl(k_sort_tiles, dim3(sort_map.unit[M] + z.blocks), dim3(1024), 0, s, sort_map, a.ids, a.id64, a.V, a.keys[0],
-             a.status, G, z);
   int at = 0;
-  int64_t run = kSortTile;
-  for (int i = 1; i <= merges; ++i, run *= 16, at ^= 1) {
-    z.from = z.to;
-    z.to = i == merges ? 1024 : 1024 * (i + 1) / (merges + 1);
+  if (longest <= kSortTile) {
+    const RowMap tiles = make_map(start, M, kSortTile);
     count_launch();
-    launch_pdl(k_merge, dim3((unsigned)((N + 1023LL) / 1024) + z.blocks), dim3(1024), 0, s, sort_map, run,
-               (const Key*)a.keys[at], a.keys[at ^ 1], G, z);
+    launch_pdl(a.V < (int64_t(1) << (32 - kPlaceBits)) ? k_sort_tiles<unsigned> : k_sort_tiles<Key>, dim3(tiles.unit[M]),
+               dim3(kSortThreads), 0, s, tiles, a.ids, a.id64, a.V, a.keys[0], a.status);
+  } else {
+    const RowMap tiles = make_map(start, M, kRadixTile);
+    int width = 1;   // bits of the ids 0 ... V
+    while (a.V >> width) ++width;
+    const int digits = (width + kDigitBits - 1) / kDigitBits, bits = (width + digits - 1) / digits;
+    count_launch();
+    launch_pdl(k_radix_count, dim3(tiles.unit[M]), dim3(256), 0, s, tiles, a.ids, a.id64, a.V, bits, digits,
+               a.counts, a.count_set, a.status);
+    for (int k = 0; k < digits; ++k) {
+      count_launch();
+      launch_pdl(k_radix_scatter, dim3(tiles.unit[M]), dim3(256), 0, s, tiles, a.ids, a.id64, a.V, k * bits, bits,
+                 k == 0 ? (const Key*)nullptr : (const Key*)a.keys[at ^ 1], a.keys[at],
+                 a.counts + k * a.count_set, k + 1 < digits ? a.counts + (k + 1) * a.count_set : (int*)nullptr);
+      at ^= 1;
+    }
+    at ^= 1;
   }
-  const RowMap map = make_map(start, M, kEmbUnit);
+  const int per_warp = embed_per_warp(N);
+  const RowMap map = make_map(start, M, 8 * per_warp);
   const int vl = a.type == LT_F32 ? 4 : 8;
   const bool vec = a.E % vl == 0 && a.ld % vl == 0 && a.off % 4 == 0 && on16(a.dY);
-#define SM_RUN(T)                                                             \
-  (vec ? run_embed_reduce<T, true>(s, a, map, longest, G, a.keys[at])         \
-       : run_embed_reduce<T, false>(s, a, map, longest, G, a.keys[at]))
+#define SM_RUN(T)                                                                     \
+  (vec ? run_embed_reduce<T, true>(s, a, map, per_warp, longest, G, a.keys[at], z)    \
+       : run_embed_reduce<T, false>(s, a, map, per_warp, longest, G, a.keys[at], z))
   if (a.type == LT_F32) SM_RUN(float);
   else if (a.type == LT_BF16) SM_RUN(__nv_bfloat16);
   else SM_RUN(__half);

@@ -116,7 +116,7 @@ def ids_of(kind, n, V, g):
     ("f32", [500, 3], 1000, 12, "falling", 1, False),
     ("bf16", [257, 3], 60, 264, "zipf", 0, True),
     ("f32", [129, 63], 5, 7, "same", 0, True),
-    ("f32", [40000, 5, 2048], 700, 4, "zipf", 0, False),     # 20 sorted tiles: two merges
+    ("f32", [40000, 5, 2048], 700, 4, "zipf", 0, False),
     ("f32", [33000], 20000, 8, "random", 0, False),
     ("bf16", [4096, 4097], 3, 16, "same", 0, False),         # one run over many units
     ("f32", [12000], 20, 16, "same", 0, False),              # ... over more than 32
@@ -124,6 +124,12 @@ def ids_of(kind, n, V, g):
     ("f32", [4678], 20, 3, "lengths", 0, False),
     ("f16", [256, 512, 255, 257], 2, 300, "random", 0, False),
     ("f32", [1, 2] * 128, 9, 5, "random", 0, False),         # 256 workers
+    ("f32", [70000], 300, 4, "zipf", 0, False),
+    ("f32", [1500, 3, 2048], (1 << 21) - 1, 1, "random", 0, False),   # the largest table of 32-bit sort keys
+    ("f32", [1500, 3, 2048], 1 << 21, 1, "random", 0, False),   # ... and one row more
+    ("bf16", [700, 9], 3, 9000, "random", 0, False),         # rows zeroed by a whole block
+    ("f32", [32768], 300, 4, "zipf", 0, False),              # the last size of small units
+    ("f32", [32769], 300, 4, "zipf", 0, False),
 ])
 def test_embed_grad(dt, rows, V, E, kind, gap, accumulate):
     n, M = sum(rows), len(rows)
@@ -153,6 +159,29 @@ def test_embed_grad(dt, rows, V, E, kind, gap, accumulate):
         again[:, 6:6 + V * E] = old
     opt.embed_grad(1, ids.int(), dY, Am, rows, scale=0.37, accumulate=accumulate)
     assert torch.equal(G, again)     # a fixed order of every sum
+
+
+@pytest.mark.parametrize("V", [400, (1 << 18) - 1, 1 << 18, (1 << 27) + 5])
+def test_embed_grad_with_one_to_four_sort_digits(V):
+    """The sort takes the bits of 0 ... V in digits of at most 9; the ids differ
+    in every one of them."""
+    n = 2500
+    opt = handle([(V, 1)], 1, n, 1)
+    g = gen(V)
+    ids = torch.randint(0, V, (n,), generator=g, device="cuda")
+    ids[:1500] = ids[1000:].clone()   # several tokens a row
+    ids[::11] = -1
+    ids[5], ids[6] = 0, V - 1
+    dY = torch.randn(n, 1, generator=g, device="cuda")
+    G, Gm = grads(opt)
+    opt.embed_grad(0, ids, dY, Gm)
+    opt.layers_sync()
+    keep = ids >= 0
+    want = torch.zeros(V, dtype=torch.float64, device="cuda").index_add_(0, ids[keep], dY[keep, 0].double())
+    size = torch.zeros(V, dtype=torch.float64, device="cuda").index_add_(0, ids[keep], dY[keep, 0].double().abs())
+    count = torch.bincount(ids[keep], minlength=V)
+    assert bool(((G[0, :V] - want).abs() <= size * (count + 2) * U).all())
+    assert bool((G[0, V:] == MARK).all())
 
 
 def test_embed_grad_skips_and_reports_ids_beyond_the_table():
