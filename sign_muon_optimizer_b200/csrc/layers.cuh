@@ -251,10 +251,15 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) 
 constexpr int kSortTile = 2048;   // tokens of a worker that one block sorts
 constexpr int kRadixTile = 2048;  // ... and that a block of the radix sort takes
 constexpr int kRadixBins = 512, kRadixSets = 4;
-// sorted tokens that a warp of the table gradient's reduction takes (a unit is
-// eight warps'): few tokens are spread over more blocks
-constexpr int64_t kFewRows = 32768;
-inline int embed_per_warp(int64_t rows) { return rows <= kFewRows ? 8 : 32; }
+// Sorted tokens that a warp of the table gradient's reduction takes (a unit is
+// eight warps'): where 32 would leave most of the SMs idle, 8 -- 9000 tokens x
+// 64 columns take 5.4 us instead of 12.7, but 9001 x 1001 take 34 instead of
+// 31 beside 116 MB of zeros.
+constexpr int kFewBlocks = 64;
+inline int embed_per_warp(int64_t rows, int64_t cols, int type) {
+  const int64_t strip = type == LT_F32 ? 128 : 256;
+  return rows / 256 * ((cols + strip - 1) / strip) <= kFewBlocks ? 8 : 32;
+}
 
 void launch_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const void* ids, int id64, int64_t n,
                   float scale, void* out, int type, int64_t ld, int* status);

@@ -111,7 +111,8 @@ int norm_blocks(signmuon_t h) { return h->n_sm * 8 + h->M; }
 // workspace layout, in bytes: embed_grad has two key arrays, digit counts and
 // the parts of cut runs, layernorm_grad the blocks' sums, distill the rows' losses
 int64_t embed_units(signmuon_t h, int64_t rows) {
-  const int64_t few = rows < sm::kFewRows ? rows : sm::kFewRows, a = few / 64, b = rows / 256;   // (8 * embed_per_warp)
+  const int64_t most = (sm::kFewBlocks + 1) * 256;   // rows that may go in units of 64
+  const int64_t a = (rows < most ? rows : most) / 64, b = rows / 256;
   return (a > b ? a : b) + h->M + 1;
 }
 int64_t count_set(signmuon_t h, int64_t rows) { return (rows / sm::kRadixTile + h->M + 1) * sm::kRadixBins; }

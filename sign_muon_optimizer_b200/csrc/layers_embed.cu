@@ -351,7 +351,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
                                                       const T* __restrict__ dY, int64_t ld, int E, int n_strip,
                                                       int64_t off, float scale, int accumulate,
-                                                      float* __restrict__ part, int per_warp, const ZeroRows zero) {
+                                                      float* __restrict__ part, int per_warp, int every,
+                                                      const ZeroRows zero) {
   constexpr int VL = Elem<T>::V;
   constexpr int AHEAD = VEC ? 4 : 8;              // rows in a batch
   constexpr int BATCHES = 3;                      // VEC: batches on their way
@@ -361,12 +362,14 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int u = blockIdx.x / n_strip;
-  if (u >= map.unit[map.M]) {
-    zero_rows(map, G, keys, E, zero, blockIdx.x - map.unit[map.M] * n_strip, reinterpret_cast<unsigned char*>(head));
+  // every `every`-th block reduces, so that reads and zeros mix throughout
+  const int sums = map.unit[map.M] * n_strip, turn = blockIdx.x / every;
+  if (blockIdx.x - turn * every != 0 || turn >= sums) {
+    zero_rows(map, G, keys, E, zero, blockIdx.x - min(sums, turn + 1), reinterpret_cast<unsigned char*>(head));
     return;
   }
-  const int c = (blockIdx.x - u * n_strip) * 32 * VL;
+  const int u = turn / n_strip;
+  const int c = (turn - u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
   const int s0 = map.start[m], s1 = map.start[m + 1];
   const int i0 = s0 + ((u - map.unit[m]) * 8 + w) * per_warp;
@@ -514,14 +517,15 @@ template <typename T, bool VEC>
 void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, int per_warp, int64_t longest,
                       const GradPtrs& G, const Key* keys, const ZeroRows& zero) {
   const int n_strip = (int)((a.E + 32 * Elem<T>::V - 1) / (32 * Elem<T>::V));
-  const int64_t blocks = (int64_t)map.unit[map.M] * n_strip;
+  const int64_t blocks = (int64_t)map.unit[map.M] * n_strip, zeros = (int64_t)zero.M * zero.groups;
+  const int every = zeros >= blocks ? 2 : 1;
   auto* reduce = k_embed_reduce<T, VEC>;
   const size_t smem = VEC ? 8 * 3 * 4 * 32 * 16 : 0;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)reduce, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   count_launch();
-  launch_pdl(reduce, dim3((unsigned)(blocks + (int64_t)zero.M * zero.groups)), dim3(256), smem, s, map, G, keys,
+  launch_pdl(reduce, dim3((unsigned)(blocks + zeros)), dim3(256), smem, s, map, G, keys,
              reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part, per_warp,
-             zero);
+             every, zero);
   if (longest <= 8 * per_warp) return;   // no run leaves its unit
   count_launch();
   launch_pdl(k_embed_join<T, VEC>, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, map, G, keys, (int)a.E, n_strip,
@@ -600,7 +604,7 @@ void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start,
     }
     at ^= 1;
   }
-  const int per_warp = embed_per_warp(N);
+  const int per_warp = embed_per_warp(N, a.E, a.type);
   const RowMap map = make_map(start, M, 8 * per_warp);
   const int vl = a.type == LT_F32 ? 4 : 8;
   const bool vec = a.E % vl == 0 && a.ld % vl == 0 && a.off % 4 == 0 && on16(a.dY);

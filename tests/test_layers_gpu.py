@@ -128,8 +128,8 @@ def ids_of(kind, n, V, g):
     ("f32", [1500, 3, 2048], (1 << 21) - 1, 1, "random", 0, False),   # the largest table of 32-bit sort keys
     ("f32", [1500, 3, 2048], 1 << 21, 1, "random", 0, False),   # ... and one row more
     ("bf16", [700, 9], 3, 9000, "random", 0, False),         # rows zeroed by a whole block
-    ("f32", [32768], 300, 4, "zipf", 0, False),              # the last size of small units
-    ("f32", [32769], 300, 4, "zipf", 0, False),
+    ("f32", [16639], 300, 4, "zipf", 0, False),              # the last size of small units
+    ("f32", [16640], 300, 4, "zipf", 0, False),
 ])
 def test_embed_grad(dt, rows, V, E, kind, gap, accumulate):
     n, M = sum(rows), len(rows)
