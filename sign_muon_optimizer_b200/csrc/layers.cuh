@@ -173,6 +173,13 @@ __device__ __forceinline__ void strip_store_f32(float* row, int base, int cols, 
   }
 }
 
+// 2^x, below 2^-126 zero
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
