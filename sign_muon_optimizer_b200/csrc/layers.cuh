@@ -61,6 +61,60 @@ struct alignas(16) Pack {
   T v[Elem<T>::V];
 };
 
+// Pairs of fp32 operations in one instruction: the kernels over rows are bound
+// by the instructions they issue as much as by the bytes.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  const float2 f = unpack2(a);
+  return f.x + f.y;
+}
+
+// elements 2j and 2j + 1 of a pack as floats, and back
+__device__ __forceinline__ F2 up2(const Pack<float>& p, int j) { return pack2(p.v[2 * j], p.v[2 * j + 1]); }
+__device__ __forceinline__ F2 up2(const Pack<__nv_bfloat16>& p, int j) {
+  const unsigned u = reinterpret_cast<const unsigned*>(p.v)[j];
+  return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ F2 up2(const Pack<__half>& p, int j) {
+  const float2 f = __half22float2(reinterpret_cast<const __half2*>(p.v)[j]);
+  return pack2(f.x, f.y);
+}
+__device__ __forceinline__ void down2(Pack<float>& p, int j, float x, float y) {
+  p.v[2 * j] = x;
+  p.v[2 * j + 1] = y;
+}
+__device__ __forceinline__ void down2(Pack<__nv_bfloat16>& p, int j, float x, float y) {
+  reinterpret_cast<__nv_bfloat162*>(p.v)[j] = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void down2(Pack<__half>& p, int j, float x, float y) {
+  reinterpret_cast<__half2*>(p.v)[j] = __floats2half2_rn(x, y);
+}
+
 // A strip is what a warp's 32 lanes hold of a row in one step: 32 * V
 // elements.  With VEC a lane holds V neighbours (one 16-byte access; the row
 // starts on 16 bytes and its length is a multiple of V), else element j of the
@@ -98,7 +152,7 @@ __device__ __forceinline__ void strip_store(T* __restrict__ row, int base, int c
     if (c < cols) {
       Pack<T> p;
 #pragma unroll
-      for (int j = 0; j < V; ++j) p.v[j] = Elem<T>::down(x[j]);
+      for (int j = 0; j < V / 2; ++j) down2(p, j, x[2 * j], x[2 * j + 1]);
       *reinterpret_cast<Pack<T>*>(row + c) = p;
     }
   } else {
@@ -189,39 +243,6 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
-}
-
-// Pairs of fp32 operations in one instruction: the kernels over rows are bound
-// by the instructions they issue as much as by the bytes.
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 pack2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float sum2(F2 a) {
-  const float2 f = unpack2(a);
-  return f.x + f.y;
 }
 
 // Asynchronous copies of 16 bytes that only the copying thread reads back:

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS)
   auto take = [&](const Pack<T>& p, F2 neg_m, F2& sum) {
 #pragma unroll
     for (int j = 0; j < VL; j += 2) {
-      const float2 x = unpack2(mul2(add2(pack2(Elem<T>::up(p.v[j]), Elem<T>::up(p.v[j + 1])), neg_m), c2));
+      const float2 x = unpack2(mul2(add2(up2(p, j / 2), neg_m), c2));
       sum = add2(pack2(ex2(x.x), ex2(x.y)), sum);
     }
   };
@@ -209,10 +209,9 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS)
     Pack<T> o;
 #pragma unroll
     for (int j = 0; j < VL; j += 2) {
-      const float2 x = unpack2(fma2(add2(pack2(Elem<T>::up(p.v[j]), Elem<T>::up(p.v[j + 1])), neg_all), c2, neg_log));
+      const float2 x = unpack2(fma2(add2(up2(p, j / 2), neg_all), c2, neg_log));
       const float2 y = unpack2(mul2(pack2(ex2(x.x), ex2(x.y)), w2));
-      o.v[j] = Elem<T>::down(y.x);
-      o.v[j + 1] = Elem<T>::down(y.y);
+      down2(o, j / 2, y.x, y.y);
     }
     T* to = dz + head + (int64_t)at * VL;
     if (vec_out) {

@@ -381,9 +381,10 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
   if (lane == 0) first_id[w] = id;
   if (w == 7 && lane == 0) first_id[8] = after;
   float* gm = G.p[m] + off;
+  F2 sum[VL / 2];
   float acc[VL];
 #pragma unroll
-  for (int j = 0; j < VL; ++j) acc[j] = 0.f;
+  for (int j = 0; j < VL / 2; ++j) sum[j] = 0ull;
   bool at_head = true;                            // still in the warp's first run
   unsigned goes_on = kAbsent;                     // the id of the run in tail[w]
   // the absent tokens are the last ones
@@ -422,10 +423,17 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
       if (k + a >= real) break;
       const unsigned v = __shfl_sync(0xffffffffu, id, k + a);
 #pragma unroll
-      for (int j = 0; j < VL; ++j) acc[j] += Elem<T>::up(raw[a].v[j]);
+      for (int j = 0; j < VL / 2; ++j) sum[j] = add2(sum[j], up2(raw[a], j));
       const bool last = k + a == per_warp - 1;
       const unsigned next = last ? after : __shfl_sync(0xffffffffu, id, (k + a + 1) & 31);
       if (next != v || last) {
+#pragma unroll
+        for (int j = 0; j < VL / 2; ++j) {
+          const float2 t = unpack2(sum[j]);
+          acc[2 * j] = t.x;
+          acc[2 * j + 1] = t.y;
+          sum[j] = 0ull;
+        }
         if (at_head && before == v) {             // (a run over the whole warp too)
 #pragma unroll
           for (int j = 0; j < VL; ++j) head[w][j][lane] = acc[j];
@@ -437,8 +445,6 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
           emit<T, VEC>(gm + (int64_t)v * E, c, E, lane, acc, scale, accumulate);
         }
         at_head = false;
-#pragma unroll
-        for (int j = 0; j < VL; ++j) acc[j] = 0.f;
       }
     }
   }

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
       else p = strip_raw<T, VEC>(X + r * ldx, (c * WPR + w) * 32 * VL, E, lane);
 #pragma unroll
       for (int j = 0; j < VL / 2; ++j) {
-        x[c][j] = pack2(Elem<T>::up(p.v[2 * j]), Elem<T>::up(p.v[2 * j + 1]));
+        x[c][j] = up2(p, j);
         a = add2(x[c][j], a);
       }
     }

@@ -114,9 +114,8 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
       }
 #pragma unroll
       for (int j = 0; j < VL / 2; ++j) {
-        const F2 x = pack2(Elem<T>::up(px.v[2 * j]), Elem<T>::up(px.v[2 * j + 1]));
-        dc[j] = pack2(Elem<T>::up(pd.v[2 * j]), Elem<T>::up(pd.v[2 * j + 1]));
-        hc[j] = mul2(add2(x, neg_mu), rs2);
+        dc[j] = up2(pd, j);
+        hc[j] = mul2(add2(up2(px, j), neg_mu), rs2);
         gc[j] = mul2(dc[j], gamma_c[j]);
       }
     };
