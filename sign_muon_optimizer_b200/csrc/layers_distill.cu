@@ -25,18 +25,27 @@ struct Teacher {
   int K;
 };
 
-// count[m] += rows of worker m with an entry that counts (a warp per row)
-__global__ void __launch_bounds__(256) k_distill_count(const RowMap map, const Teacher te, int64_t V, int* count) {
+// count[m] += rows of worker m with an entry that counts: a warp per row, one
+// addition per block and worker
+__global__ void __launch_bounds__(1024) k_distill_count(const RowMap map, const Teacher te, int64_t V, int* count) {
+  __shared__ int any_of[32];
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= map.start[map.M]) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t r = (int64_t)blockIdx.x * 32 + w;
   bool any = false;
-  for (int k = lane; k < te.K; k += 32)
-    any |= counts(load_id(te.idx, te.id64, (int64_t)r * te.ldt + k), V, load_t(te.t, te.t_type, (int64_t)r * te.ldt + k));
+  if (r < map.start[map.M])
+    for (int k = lane; k < te.K; k += 32)
+      any |= counts(load_id(te.idx, te.id64, r * te.ldt + k), V, load_t(te.t, te.t_type, r * te.ldt + k));
   any = __any_sync(0xffffffffu, any);
-  if (lane == 0 && any) atomicAdd(&count[worker_of(map.start, map.M, r)], 1);
+  if (lane == 0) any_of[w] = any;
+  __syncthreads();
+  if (w != 0) return;
+  // lane i: row i of the block
+  const int64_t mine = (int64_t)blockIdx.x * 32 + lane;
+  const int m = any_of[lane] ? worker_of(map.start, map.M, (int)mine) : -1;
+  const unsigned same = __match_any_sync(0xffffffffu, m);
+  if (m >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[m], __popc(same));
 }
 
 // the maximum of a 16-byte pack, as a float (a NaN does not count)
@@ -71,178 +80,365 @@ struct Running {
   }
 };
 
-// ROW_THREADS threads hold a row: a block, or a warp (four rows a block).  The
-// row is read twice, for the maximum and sum of the softmax and for the
-// gradient (the second time from L2).  Every warp works out the teacher's
-// softmax for itself, the first one leaves its entries in shared memory.
-template <typename T, int ROW_THREADS>
-__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS)
-    k_distill_rows(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, float temperature,
-                   float gscale, int* count, int count_here, float* __restrict__ row_loss, T* dZ, int64_t ldd,
-                   int* status) {
+// A row's logits as whole 16-byte packs between a head and a tail.
+template <typename T>
+struct RowView {
+  const T* z;
+  int mis, head, nv, tail, n_tail;   // tail = head + nv * V; n_tail elements from there on
+  __device__ __forceinline__ RowView(const T* row, int64_t V) : z(row) {
+    constexpr int VL = Elem<T>::V;
+    mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    head = (int)(V < (VL - mis) % VL ? V : (VL - mis) % VL);
+    nv = (int)((V - head) / VL);
+    tail = head + nv * VL;
+    n_tail = (int)(V - tail);
+  }
+  __device__ __forceinline__ const Pack<T>* packs() const { return reinterpret_cast<const Pack<T>*>(z + head); }
+};
+
+constexpr int kAhead = 4;   // packs loaded before the first is used
+
+// Pass 1: packs tid, tid + THREADS, ... of a row into the running softmax;
+// after(i) follows when pack i is done.
+template <typename T, int THREADS, typename F>
+__device__ __forceinline__ void absorb(Running& run, const Pack<T>* packs, int nv, int tid, float c, F after) {
   constexpr int VL = Elem<T>::V;
-  constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
-  constexpr int AHEAD = 4;                        // packs loaded before the first is used
-  extern __shared__ float entries[];              // per row: q, z and index of the K entries
-  __shared__ float2 buf[WARPS];
-  griddep_wait();
-  griddep_launch();
-  const int K = te.K;
-  const int lane = threadIdx.x & 31, tid = threadIdx.x % ROW_THREADS;
-  const int in_block = threadIdx.x / ROW_THREADS;
-  const int r = blockIdx.x * ROWS + in_block;
-  if (r >= map.start[map.M]) return;              // (a whole warp)
-  float* q = entries + (int64_t)in_block * 3 * K;
-  float* zk = q + K;
-  int* id = reinterpret_cast<int*>(q + 2 * K);
-  auto sync = [&] {
-    if (ROW_THREADS == 32) __syncwarp();
-    else __syncthreads();
-  };
-  const T* z = Z + (int64_t)r * ldz;
-  T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
-  const int m = worker_of(map.start, map.M, r);
-  // the teacher's softmax
-  const float inv_T = 1.f / temperature;
-  float top = -INFINITY;
-  bool any = false;
-  for (int k = lane; k < K; k += 32) {
-    const int64_t i = load_id(te.idx, te.id64, (int64_t)r * te.ldt + k);
-    const float t = load_t(te.t, te.t_type, (int64_t)r * te.ldt + k);
-    const bool c = counts(i, V, t);
-    any |= c;
-    if (c) top = fmaxf(top, t);
-    if (tid < 32) {
-      if (i >= V) *status = 1;
-      id[k] = c ? (int)i : -1;
-      q[k] = t;
-      if (c) zk[k] = Elem<T>::up(z[i]);
-    }
-  }
-  if (!__any_sync(0xffffffffu, any)) {            // the same in every warp of the row
-    if (dz != nullptr)
-      for (int64_t v = tid; v < V; v += ROW_THREADS) dz[v] = Elem<T>::down(0.f);
-    if (tid == 0) row_loss[r] = 0.f;
-    return;
-  }
-  if (count_here && tid == 0) atomicAdd(&count[m], 1);
-  top = warp_max(top);
-  // the student's maximum and sum: whole 16-byte packs between a head and a tail
-  const float c = inv_T * 1.4426950408889634f;
-  const int mis = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
-  const int head = (int)(V < (VL - mis) % VL ? V : (VL - mis) % VL);
-  const int nv = (int)((V - head) / VL);
-  const int tail = head + nv * VL, n_tail = (int)(V - tail);
-  const Pack<T>* zp = reinterpret_cast<const Pack<T>*>(z + head);
-  Running run;
   const F2 c2 = pack2(c, c);
   auto take = [&](const Pack<T>& p, F2 neg_m, F2& sum) {
 #pragma unroll
-    for (int j = 0; j < VL; j += 2) {
-      const float2 x = unpack2(mul2(add2(up2(p, j / 2), neg_m), c2));
+    for (int j = 0; j < VL / 2; ++j) {
+      const float2 x = unpack2(mul2(add2(up2(p, j), neg_m), c2));
       sum = add2(pack2(ex2(x.x), ex2(x.y)), sum);
     }
   };
   int i = tid;
-  for (; i + (AHEAD - 1) * ROW_THREADS < nv; i += AHEAD * ROW_THREADS) {
-    Pack<T> p[AHEAD];
+  for (; i + (kAhead - 1) * THREADS < nv; i += kAhead * THREADS) {
+    Pack<T> p[kAhead];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) p[a] = zp[i + a * ROW_THREADS];
+    for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * THREADS];
     float t = pack_max(p[0]);
 #pragma unroll
-    for (int a = 1; a < AHEAD; ++a) t = fmaxf(t, pack_max(p[a]));
+    for (int a = 1; a < kAhead; ++a) t = fmaxf(t, pack_max(p[a]));
     run.raise(t, c);
     const float neg = -Running::ref(run.m);
     F2 sum = 0ull;
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) take(p[a], pack2(neg, neg), sum);
+    for (int a = 0; a < kAhead; ++a) take(p[a], pack2(neg, neg), sum);
     run.s += sum2(sum);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) after(i + a * THREADS);
   }
-  for (; i < nv; i += ROW_THREADS) {
-    const Pack<T> p = zp[i];
+  for (; i < nv; i += THREADS) {
+    const Pack<T> p = packs[i];
     run.raise(pack_max(p), c);
     const float neg = -Running::ref(run.m);
     F2 sum = 0ull;
     take(p, pack2(neg, neg), sum);
     run.s += sum2(sum);
+    after(i);
   }
-  if (tid < head) run.one(Elem<T>::up(z[tid]), c);
-  if (tid < n_tail) run.one(Elem<T>::up(z[tail + tid]), c);
-  // over the row's threads (a sum without a finite logit is 0 or NaN and is kept)
-  float all = warp_max(run.m);
-  float s = warp_sum(run.m == -INFINITY ? run.s : run.s * ex2((run.m - all) * c));
-  if (ROW_THREADS > 32) {
-    if (lane == 0) buf[tid >> 5] = make_float2(all, s);
-    __syncthreads();
-    const float2 b = lane < WARPS ? buf[lane] : make_float2(-INFINITY, 0.f);
+}
+
+// The row's maximum and sum from its threads' (a sum without a finite logit is
+// 0 or NaN and is kept); WARPS > 1: buf has a float2 per warp, and the block
+// passes a barrier.
+template <int WARPS, typename F>
+__device__ __forceinline__ void join_row(const Running& run, int tid, float c, float2* buf, F barrier, float& all, float& s) {
+  all = warp_max(run.m);
+  s = warp_sum(run.m == -INFINITY ? run.s : run.s * ex2((run.m - all) * c));
+  if (WARPS > 1) {
+    if ((tid & 31) == 0) buf[tid >> 5] = make_float2(all, s);
+    barrier();
+    const float2 b = (tid & 31) < WARPS ? buf[tid & 31] : make_float2(-INFINITY, 0.f);
     all = warp_max(b.x);
     s = warp_sum(b.x == -INFINITY ? b.y : b.y * ex2((b.x - all) * c));
-  } else {
-    __syncwarp();
   }
-  const float log2_s = log2f(s);
-  if (tid < 32) {
-    // the row's loss, and the teacher's probabilities
-    float sum = 0.f;
-    for (int k = lane; k < K; k += 32)
-      if (id[k] >= 0) sum += expf((q[k] - top) * inv_T);
-    const float log_sum_t = logf(warp_sum(sum));
-    const float log_s = log2_s * 0.6931471805599453f;
-    float loss = 0.f;
-    for (int k = lane; k < K; k += 32) {
-      if (id[k] < 0) continue;
-      const float lq = (q[k] - top) * inv_T - log_sum_t;
-      const float qk = expf(lq);
-      if (!(qk == 0.f)) loss += qk * (lq - ((zk[k] - all) * inv_T - log_s));
-      q[k] = qk;
-    }
-    loss = warp_sum(loss);
-    if (tid == 0) row_loss[r] = loss * (temperature * temperature);
-  }
-  if (dz == nullptr) return;
-  // the gradient: w * p everywhere, then the teacher's entries
-  const float w = gscale * temperature / (float)count[m];
-  const F2 neg_all = pack2(-all, -all), neg_log = pack2(-log2_s, -log2_s), w2 = pack2(w, w);
-  const bool vec_out = ((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T)) == mis;
-  auto grad = [&](float x) { return Elem<T>::down(w * ex2(fmaf(x - all, c, -log2_s))); };
-  auto give = [&](const Pack<T>& p, int at) {
+}
+
+// Pass 2: dz = w * p, p = 2^((z - all) c - log2 s), of packs tid, tid + THREADS, ...
+template <typename T>
+struct Gradient {
+  float all, c, log2_s, w;
+  __device__ __forceinline__ float p(float z) const { return ex2(fmaf(z - all, c, -log2_s)); }
+  __device__ __forceinline__ T one(float z) const { return Elem<T>::down(w * p(z)); }
+  __device__ __forceinline__ void pack(const Pack<T>& z, T* to, bool aligned) const {
+    constexpr int VL = Elem<T>::V;
+    const F2 neg_all = pack2(-all, -all), neg_log = pack2(-log2_s, -log2_s), w2 = pack2(w, w), c2 = pack2(c, c);
     Pack<T> o;
 #pragma unroll
-    for (int j = 0; j < VL; j += 2) {
-      const float2 x = unpack2(fma2(add2(up2(p, j / 2), neg_all), c2, neg_log));
+    for (int j = 0; j < VL / 2; ++j) {
+      const float2 x = unpack2(fma2(add2(up2(z, j), neg_all), c2, neg_log));
       const float2 y = unpack2(mul2(pack2(ex2(x.x), ex2(x.y)), w2));
-      down2(o, j / 2, y.x, y.y);
+      down2(o, j, y.x, y.y);
     }
-    T* to = dz + head + (int64_t)at * VL;
-    if (vec_out) {
+    store(o, to, aligned);
+  }
+  static __device__ __forceinline__ void store(const Pack<T>& o, T* to, bool aligned) {
+    if (aligned) {
       *reinterpret_cast<Pack<T>*>(to) = o;
     } else {
 #pragma unroll
-      for (int j = 0; j < VL; ++j) to[j] = o.v[j];
+      for (int j = 0; j < Elem<T>::V; ++j) to[j] = o.v[j];
     }
-  };
-  i = tid;
-  for (; i + (AHEAD - 1) * ROW_THREADS < nv; i += AHEAD * ROW_THREADS) {
-    Pack<T> p[AHEAD];
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) p[a] = zp[i + a * ROW_THREADS];
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) give(p[a], i + a * ROW_THREADS);
   }
-  for (; i < nv; i += ROW_THREADS) give(zp[i], i);
-  if (tid < head) dz[tid] = grad(Elem<T>::up(z[tid]));
-  if (tid < n_tail) dz[tail + tid] = grad(Elem<T>::up(z[tail + tid]));
-  sync();
-  for (int k = tid; k < K; k += ROW_THREADS) {
-    if (id[k] < 0) continue;
-    bool mine = true;   // the first of the entries with this index writes for all of them
-    float sum_q = 0.f;
-    for (int e = 0; e < K; ++e)
-      if (id[e] == id[k]) {
-        if (e < k) mine = false;
-        sum_q += q[e];
+};
+
+// The teacher's entries of a row in shared memory, K of each.
+struct Entries {
+  float *q, *lq, *zk;   // probability, its logarithm, the student's logit there
+  int* id;              // -1: absent
+  __device__ __forceinline__ Entries(float* at, int K)
+      : q(at), lq(at + K), zk(at + 2 * K), id(reinterpret_cast<int*>(at + 3 * K)) {}
+};
+
+// one warp: row r's entries; true if one counts
+template <typename T>
+__device__ __forceinline__ bool read_teacher(const Teacher& te, int r, const T* z, int64_t V, float inv_T,
+                                             const Entries& e, int* status) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  bool any = false;
+  for (int k = lane; k < te.K; k += 32) {
+    const int64_t i = load_id(te.idx, te.id64, (int64_t)r * te.ldt + k);
+    const float t = load_t(te.t, te.t_type, (int64_t)r * te.ldt + k);
+    if (i >= V) *status = 1;
+    const bool c = counts(i, V, t);
+    any |= c;
+    e.id[k] = c ? (int)i : -1;
+    e.lq[k] = t;
+    if (c) {
+      top = fmaxf(top, t);
+      e.zk[k] = Elem<T>::up(z[i]);
+    }
+  }
+  if (!__any_sync(0xffffffffu, any)) return false;
+  top = warp_max(top);
+  float sum = 0.f;
+  for (int k = lane; k < te.K; k += 32)
+    if (e.id[k] >= 0) sum += expf((e.lq[k] - top) * inv_T);
+  const float log_sum = logf(warp_sum(sum));
+  for (int k = lane; k < te.K; k += 32) {
+    if (e.id[k] < 0) continue;
+    const float lq = (e.lq[k] - top) * inv_T - log_sum;
+    e.lq[k] = lq;
+    e.q[k] = expf(lq);
+  }
+  __syncwarp();
+  return true;
+}
+
+// one warp: T^2 * sum of q (log q - log p); lane 0 has it
+__device__ __forceinline__ float row_loss_of(const Entries& e, int K, float all, float log2_s, float inv_T, float T) {
+  const float log_s = log2_s * 0.6931471805599453f;
+  float loss = 0.f;
+  for (int k = threadIdx.x & 31; k < K; k += 32)
+    if (e.id[k] >= 0 && !(e.q[k] == 0.f)) loss += e.q[k] * (e.lq[k] - ((e.zk[k] - all) * inv_T - log_s));
+  return warp_sum(loss) * (T * T);
+}
+
+// thread tid of THREADS: the gradient at the teacher's entries.  The first of
+// the entries with the same index writes for all of them.
+template <typename T>
+__device__ __forceinline__ void correct(const Entries& e, int K, int tid, int threads, const Gradient<T>& g, T* dz) {
+  for (int k = tid; k < K; k += threads) {
+    if (e.id[k] < 0) continue;
+    bool mine = true;
+    float sum = 0.f;
+    for (int i = 0; i < K; ++i)
+      if (e.id[i] == e.id[k]) {
+        if (i < k) mine = false;
+        sum += e.q[i];
       }
-    if (mine) dz[id[k]] = Elem<T>::down(w * (ex2(fmaf(zk[k] - all, c, -log2_s)) - sum_q));
+    if (mine) dz[e.id[k]] = Elem<T>::down(g.w * (g.p(e.zk[k]) - sum));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_row(T* dz, int64_t V, int tid, int threads) {
+  const RowView<T> v(dz, V);
+  Pack<T> o;
+#pragma unroll
+  for (int j = 0; j < Elem<T>::V; ++j) o.v[j] = Elem<T>::down(0.f);
+  for (int i = tid; i < v.nv; i += threads) *reinterpret_cast<Pack<T>*>(dz + v.head + (int64_t)i * Elem<T>::V) = o;
+  if (tid < v.head) dz[tid] = o.v[0];
+  if (tid < v.n_tail) dz[v.tail + tid] = o.v[0];
+}
+
+// ROW_THREADS threads hold a row: a block (rows too long for shared memory), or
+// a warp (short rows, four a block).  The row is read twice, for the maximum
+// and sum of the softmax and for the gradient (the second time from L2).
+template <typename T, int ROW_THREADS>
+__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THREADS == 32 ? 8 : 2)
+    k_distill_rows(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, float temperature,
+                   float gscale, int* count, int count_here, float* __restrict__ row_loss, T* dZ, int64_t ldd,
+                   int* status) {
+  constexpr int VL = Elem<T>::V;
+  constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
+  extern __shared__ float entries[];              // per row: 4 arrays of K
+  __shared__ float2 buf[WARPS];
+  __shared__ int some[ROWS];
+  griddep_wait();
+  griddep_launch();
+  const int tid = threadIdx.x % ROW_THREADS, in_block = threadIdx.x / ROW_THREADS;
+  const int r = blockIdx.x * ROWS + in_block;
+  if (r >= map.start[map.M]) return;              // (a whole warp)
+  const Entries e(entries + (int64_t)in_block * 4 * te.K, te.K);
+  auto sync = [&] {
+    if (ROW_THREADS == 32) __syncwarp();
+    else __syncthreads();
+  };
+  const int m = worker_of(map.start, map.M, r);
+  const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
+  const RowView<T> v(Z + (int64_t)r * ldz, V);
+  if (tid < 32) {
+    const bool any = read_teacher(te, r, v.z, V, inv_T, e, status);
+    if (tid == 0) {
+      some[in_block] = any;
+      if (any && count_here) atomicAdd(&count[m], 1);
+      if (!any) row_loss[r] = 0.f;
+    }
+  }
+  sync();
+  T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
+  if (!some[in_block]) {
+    if (dz != nullptr) zero_row(dz, V, tid, ROW_THREADS);
+    return;
+  }
+  Running run;
+  absorb<T, ROW_THREADS>(run, v.packs(), v.nv, tid, c, [](int) {});
+  if (tid < v.head) run.one(Elem<T>::up(v.z[tid]), c);
+  if (tid < v.n_tail) run.one(Elem<T>::up(v.z[v.tail + tid]), c);
+  float all, s;
+  join_row<WARPS>(run, tid, c, buf, sync, all, s);
+  const float log2_s = log2f(s);
+  if (tid < 32) {
+    const float loss = row_loss_of(e, te.K, all, log2_s, inv_T, temperature);
+    if (tid == 0) row_loss[r] = loss;
+  }
+  if (dz == nullptr) return;
+  const Gradient<T> g{all, c, log2_s, gscale * temperature / (float)count[m]};
+  const bool aligned = RowView<T>(dz, V).mis == v.mis;
+  const Pack<T>* packs = v.packs();
+  T* out = dz + v.head;
+  int i = tid;
+  for (; i + (kAhead - 1) * ROW_THREADS < v.nv; i += kAhead * ROW_THREADS) {
+    Pack<T> p[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * ROW_THREADS];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) g.pack(p[a], out + (int64_t)(i + a * ROW_THREADS) * VL, aligned);
+  }
+  for (; i < v.nv; i += ROW_THREADS) g.pack(packs[i], out + (int64_t)i * VL, aligned);
+  if (tid < v.head) dz[tid] = g.one(Elem<T>::up(v.z[tid]));
+  if (tid < v.n_tail) dz[v.tail + tid] = g.one(Elem<T>::up(v.z[v.tail + tid]));
+  sync();
+  correct(e, te.K, tid, ROW_THREADS, g, dz);
+}
+
+// A block stays and takes row after row, each in shared memory: the next row
+// comes in through asynchronous copies while this one's gradient goes out (or,
+// for the loss alone, while its sum is made), pack by pack into the places that
+// the same thread has just read.  One more warp works ahead on the teacher's
+// entries of the next row and does the loss.  Two blocks on an SM.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
+    k_distill_resident(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, int slots,
+                       float temperature, float gscale, int* count, int count_here, float* __restrict__ row_loss,
+                       T* dZ, int64_t ldd, int* status) {
+  constexpr int VL = Elem<T>::V, WARPS = THREADS / 32;
+  extern __shared__ uint4 row_at[];               // `slots` packs, then twice 4 arrays of K
+  __shared__ float2 buf[2][WARPS];
+  __shared__ int some[2];
+  griddep_wait();
+  griddep_launch();
+  float* entries = reinterpret_cast<float*>(row_at + slots);
+  const int N = map.start[map.M];
+  const int tid = threadIdx.x;
+  const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
+  const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row_at);
+  int b = 0;
+  if (tid >= THREADS) {                           // the teacher's warp
+    auto prepare = [&](int r, int to) {
+      const bool any = read_teacher(te, r, Z + (int64_t)r * ldz, V, inv_T, Entries(entries + to * 4 * te.K, te.K), status);
+      if ((tid & 31) == 0) {
+        some[to] = any;
+        if (any && count_here) atomicAdd(&count[worker_of(map.start, map.M, r)], 1);
+      }
+    };
+    prepare(blockIdx.x, 0);
+    for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
+      __syncthreads();                            // the row's maxima and sums are in buf
+      const Entries e(entries + b * 4 * te.K, te.K);
+      const bool any = some[b] != 0;
+      const float2 x = (tid & 31) < WARPS ? buf[b][tid & 31] : make_float2(-INFINITY, 0.f);
+      const float all = warp_max(x.x);
+      const float s = warp_sum(x.x == -INFINITY ? x.y : x.y * ex2((x.x - all) * c));
+      const float loss = any ? row_loss_of(e, te.K, all, log2f(s), inv_T, temperature) : 0.f;
+      if ((tid & 31) == 0) row_loss[r] = loss;
+      if (r + (int64_t)gridDim.x < N) prepare(r + gridDim.x, b ^ 1);
+    }
+    return;
+  }
+  auto fetch = [&](const RowView<T>& v, int i) {
+    if (i < v.nv) copy16(&row_at[i], v.packs() + i, true);
+  };
+  {
+    const RowView<T> v(Z + (int64_t)blockIdx.x * ldz, V);
+    for (int i = tid; i < v.nv; i += THREADS) fetch(v, i);
+  }
+  for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
+    const RowView<T> v(Z + (int64_t)r * ldz, V);
+    const bool more = r + (int64_t)gridDim.x < N;
+    RowView<T> next(Z + (int64_t)(more ? r + gridDim.x : r) * ldz, V);
+    if (!more) next.nv = 0;
+    const float edge0 = tid < v.head ? Elem<T>::up(v.z[tid]) : -INFINITY;
+    const float edge1 = tid < v.n_tail ? Elem<T>::up(v.z[v.tail + tid]) : -INFINITY;
+    const float n = dZ != nullptr ? (float)count[worker_of(map.start, map.M, r)] : 1.f;
+    copy_commit();
+    copy_wait<0>();
+    Running run;
+    if (dZ != nullptr) {
+      absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int) {});
+    } else {
+      absorb<T, THREADS>(run, packs, v.nv, tid, c, [&](int i) { fetch(next, i); });
+    }
+    if (tid < v.head) run.one(edge0, c);
+    if (tid < v.n_tail) run.one(edge1, c);
+    float all, s;
+    join_row<WARPS>(run, tid, c, buf[b], [] { __syncthreads(); }, all, s);
+    int i = tid;
+    if (dZ != nullptr) {
+      T* dz = dZ + (int64_t)r * ldd;
+      const Gradient<T> g{all, c, log2f(s), gscale * temperature / n};
+      if (some[b]) {
+        const bool aligned = RowView<T>(dz, V).mis == v.mis;
+        T* out = dz + v.head;
+        for (; i + (kAhead - 1) * THREADS < v.nv; i += kAhead * THREADS) {
+          Pack<T> p[kAhead];
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * THREADS];
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) {
+            g.pack(p[a], out + (int64_t)(i + a * THREADS) * VL, aligned);
+            fetch(next, i + a * THREADS);
+          }
+        }
+        for (; i < v.nv; i += THREADS) {
+          g.pack(packs[i], out + (int64_t)i * VL, aligned);
+          fetch(next, i);
+        }
+        if (tid < v.head) dz[tid] = g.one(edge0);
+        if (tid < v.n_tail) dz[v.tail + tid] = g.one(edge1);
+      } else {
+        zero_row(dz, V, tid, THREADS);
+      }
+      for (; i < next.nv; i += THREADS) fetch(next, i);   // packs that this row has not
+      asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");  // the row's gradient is written
+      if (some[b]) correct(Entries(entries + b * 4 * te.K, te.K), te.K, tid, THREADS, g, dz);
+    } else {
+      while (i < v.nv) i += THREADS;
+      for (; i < next.nv; i += THREADS) fetch(next, i);
+    }
   }
 }
 
@@ -272,7 +468,7 @@ __global__ void __launch_bounds__(256) k_distill_loss(const RowMap map, const fl
 template <typename T, int ROW_THREADS>
 void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1;
-  const size_t smem = (size_t)ROWS * 3 * a.K * 4;
+  const size_t smem = (size_t)ROWS * 4 * a.K * 4;
   auto* kernel = k_distill_rows<T, ROW_THREADS>;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   count_launch();
@@ -281,11 +477,35 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
              a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd, a.status);
 }
 
-// a warp for the shortest rows, so that most of it has something to load
+int resident_slots(const DistillArgs& a, int elem, int threads) {
+  const int64_t packs = a.V * elem / 16;
+  return (int)((packs + threads - 1) / threads * threads);
+}
+
+template <typename T, int THREADS>
+void run_resident(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
+  auto* kernel = k_distill_resident<T, THREADS>;
+  const int slots = resident_slots(a, sizeof(T), THREADS);
+  const size_t smem = (size_t)slots * 16 + (size_t)2 * 4 * a.K * 4;
+  cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int grid = stream_grid((const void*)kernel, THREADS + 32, smem, map.start[map.M], 16);
+  count_launch();
+  launch_pdl(kernel, dim3(grid), dim3(THREADS + 32), smem, s, map, te, reinterpret_cast<const T*>(a.Z), a.ldz, a.V,
+             slots, a.temperature, a.gscale, a.count, a.dZ == nullptr ? 1 : 0, a.row_loss, reinterpret_cast<T*>(a.dZ),
+             a.ldd, a.status);
+}
+
+// A warp for the shortest rows, so that most of it has something to load; rows
+// of which two fit an SM's shared memory stay there; longer ones are read twice.
+constexpr size_t kResidentBytes = 112 * 1024;
 template <typename T>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
+  const int64_t fixed = (int64_t)2 * 4 * a.K * 4 + 512;
   if (a.V <= 1024) run_rows<T, 32>(s, a, map, te);
-  else if (a.V <= 8192) run_rows<T, 128>(s, a, map, te);
+  else if (a.V <= 8192) run_resident<T, 128>(s, a, map, te);
+  else if (a.V * (int64_t)sizeof(T) + 16 * 512 + fixed <= (int64_t)kResidentBytes &&
+           (int64_t)resident_slots(a, sizeof(T), 512) * 16 + fixed <= (int64_t)kResidentBytes)
+    run_resident<T, 512>(s, a, map, te);
   else run_rows<T, 512>(s, a, map, te);
 }
 
@@ -301,7 +521,7 @@ void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int 
     // the gradient needs the worker's row count before its first row is done
     if (a.dZ != nullptr) {
       count_launch();
-      launch_pdl(k_distill_count, dim3((unsigned)((N + 7LL) / 8)), dim3(256), 0, s, map, te, a.V, a.count);
+      launch_pdl(k_distill_count, dim3((unsigned)((N + 31LL) / 32)), dim3(1024), 0, s, map, te, a.V, a.count);
     }
     if (a.type == LT_F32) pick_rows<float>(s, a, map, te);
     else if (a.type == LT_BF16) pick_rows<__nv_bfloat16>(s, a, map, te);
