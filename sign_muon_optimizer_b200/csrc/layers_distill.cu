@@ -63,20 +63,27 @@ __device__ __forceinline__ float pack_max(const Pack<__half>& p) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 
-// A running softmax: the maximum m of the logits so far and the sum s of
-// 2^((z - m) c).  Without a finite logit m is -inf and s is 0 (or NaN).
+// A running softmax of y = z c (c = log2 e / T): the maximum m of the logits
+// and the sum s of 2^(z c - R), with the reference R = fl(m c), one fma a term.
+// The rounding of R is common to every term and cancels in p.  R is at least
+// -1e37, so that logits of -inf or of the type's lowest value add 0 to s; rows
+// whose own maximum is out of range are `far` and done over, term by term.
+constexpr float kFar = 1e37f;
+__device__ __forceinline__ float reference(float m, float c) { return fmaxf(m * c, -kFar); }
+
 struct Running {
   float m = -INFINITY, s = 0.f;
-  __device__ __forceinline__ static float ref(float m) { return m == -INFINITY ? 0.f : m; }
-  __device__ __forceinline__ void raise(float top, float c) {
+  __device__ __forceinline__ float raise(float top, float c) {   // returns the reference
+    const float r = reference(fmaxf(m, top), c);
     if (top > m) {
-      if (m != -INFINITY) s *= ex2((m - top) * c);
+      s *= ex2(reference(m, c) - r);
       m = top;
     }
+    return r;
   }
   __device__ __forceinline__ void one(float z, float c) {
-    raise(z, c);
-    s += ex2((z - ref(m)) * c);
+    const float r = raise(z, c);
+    s += ex2(fmaf(z, c, -r));
   }
 };
 
@@ -98,90 +105,142 @@ struct RowView {
 
 constexpr int kAhead = 4;   // packs loaded before the first is used
 
-// Pass 1: packs tid, tid + THREADS, ... of a row into the running softmax;
-// after(i) follows when pack i is done.
+// Pass 1: packs tid, tid + THREADS, ... of nv into the running softmax;
+// after(i, n) follows when n packs from pack i on (THREADS apart) are done.
 template <typename T, int THREADS, typename F>
 __device__ __forceinline__ void absorb(Running& run, const Pack<T>* packs, int nv, int tid, float c, F after) {
   constexpr int VL = Elem<T>::V;
   const F2 c2 = pack2(c, c);
-  auto take = [&](const Pack<T>& p, F2 neg_m, F2& sum) {
+  auto take = [&](const Pack<T>& p, F2 neg, F2& sum) {
 #pragma unroll
     for (int j = 0; j < VL / 2; ++j) {
-      const float2 x = unpack2(mul2(add2(up2(p, j), neg_m), c2));
+      const float2 x = unpack2(fma2(up2(p, j), c2, neg));
       sum = add2(pack2(ex2(x.x), ex2(x.y)), sum);
     }
   };
   int i = tid;
   for (; i + (kAhead - 1) * THREADS < nv; i += kAhead * THREADS) {
     Pack<T> p[kAhead];
+    const Pack<T>* from = packs + i;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * THREADS];
+    for (int a = 0; a < kAhead; ++a) p[a] = from[a * THREADS];
     float t = pack_max(p[0]);
 #pragma unroll
     for (int a = 1; a < kAhead; ++a) t = fmaxf(t, pack_max(p[a]));
-    run.raise(t, c);
-    const float neg = -Running::ref(run.m);
+    const float r = run.raise(t, c);
+    const F2 neg = pack2(-r, -r);
     F2 sum = 0ull;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) take(p[a], pack2(neg, neg), sum);
+    for (int a = 0; a < kAhead; ++a) take(p[a], neg, sum);
     run.s += sum2(sum);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) after(i + a * THREADS);
+    after(i, kAhead);
   }
   for (; i < nv; i += THREADS) {
     const Pack<T> p = packs[i];
-    run.raise(pack_max(p), c);
-    const float neg = -Running::ref(run.m);
+    const float r = run.raise(pack_max(p), c);
     F2 sum = 0ull;
-    take(p, pack2(neg, neg), sum);
+    take(p, pack2(-r, -r), sum);
     run.s += sum2(sum);
-    after(i);
+    after(i, 1);
   }
 }
 
-// The row's maximum and sum from its threads' (a sum without a finite logit is
-// 0 or NaN and is kept); WARPS > 1: buf has a float2 per warp, and the block
-// passes a barrier.
+// The row's maximum and sum from its threads' (a sum that is NaN stays);
+// WARPS > 1: buf has a float2 per warp, and the block passes a barrier.
+__device__ __forceinline__ void join_lanes(float c, float& m, float& s) {
+  const float all = warp_max(m);
+  s = warp_sum(s * ex2(reference(m, c) - reference(all, c)));
+  m = all;
+}
 template <int WARPS, typename F>
 __device__ __forceinline__ void join_row(const Running& run, int tid, float c, float2* buf, F barrier, float& all, float& s) {
-  all = warp_max(run.m);
-  s = warp_sum(run.m == -INFINITY ? run.s : run.s * ex2((run.m - all) * c));
+  all = run.m;
+  s = run.s;
+  join_lanes(c, all, s);
   if (WARPS > 1) {
     if ((tid & 31) == 0) buf[tid >> 5] = make_float2(all, s);
     barrier();
     const float2 b = (tid & 31) < WARPS ? buf[tid & 31] : make_float2(-INFINITY, 0.f);
-    all = warp_max(b.x);
-    s = warp_sum(b.x == -INFINITY ? b.y : b.y * ex2((b.x - all) * c));
+    all = b.x;
+    s = b.y;
+    join_lanes(c, all, s);
   }
 }
 
-// Pass 2: dz = w * p, p = 2^((z - all) c - log2 s), of packs tid, tid + THREADS, ...
+// A row's softmax p = e(z) / s and gradient w * p.
 template <typename T>
-struct Gradient {
-  float all, c, log2_s, w;
-  __device__ __forceinline__ float p(float z) const { return ex2(fmaf(z - all, c, -log2_s)); }
-  __device__ __forceinline__ T one(float z) const { return Elem<T>::down(w * p(z)); }
-  __device__ __forceinline__ void pack(const Pack<T>& z, T* to, bool aligned) const {
-    constexpr int VL = Elem<T>::V;
-    const F2 neg_all = pack2(-all, -all), neg_log = pack2(-log2_s, -log2_s), w2 = pack2(w, w), c2 = pack2(c, c);
-    Pack<T> o;
+struct Softmax {
+  float all, c, r, s;   // r: the reference of all
+  bool far;
+  __device__ __forceinline__ Softmax(float all_, float s_, float c_)
+      : all(all_), c(c_), r(reference(all_, c_)), s(s_), far(!(fabsf(all_ * c_) <= kFar)) {}
+  // log2 of e(z); far rows subtract first
+  __device__ __forceinline__ float log2_e(float z) const { return far ? (z - all) * c : fmaf(z, c, -r); }
+  __device__ __forceinline__ T grad(float z, float w) const { return Elem<T>::down(w / s * ex2(log2_e(z))); }
+  // one pack of a row that is not far; ws = w / s
+  __device__ __forceinline__ void pack(const Pack<T>& z, float ws, Pack<T>& o) const {
+    const F2 neg = pack2(-r, -r), c2 = pack2(c, c), ws2 = pack2(ws, ws);
 #pragma unroll
-    for (int j = 0; j < VL / 2; ++j) {
-      const float2 x = unpack2(fma2(add2(up2(z, j), neg_all), c2, neg_log));
-      const float2 y = unpack2(mul2(pack2(ex2(x.x), ex2(x.y)), w2));
+    for (int j = 0; j < Elem<T>::V / 2; ++j) {
+      const float2 x = unpack2(fma2(up2(z, j), c2, neg));
+      const float2 y = unpack2(mul2(pack2(ex2(x.x), ex2(x.y)), ws2));
       down2(o, j, y.x, y.y);
-    }
-    store(o, to, aligned);
-  }
-  static __device__ __forceinline__ void store(const Pack<T>& o, T* to, bool aligned) {
-    if (aligned) {
-      *reinterpret_cast<Pack<T>*>(to) = o;
-    } else {
-#pragma unroll
-      for (int j = 0; j < Elem<T>::V; ++j) to[j] = o.v[j];
     }
   }
 };
+
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store_pack(const Pack<T>& o, T* to) {
+  if (ALIGNED) {
+    *reinterpret_cast<Pack<T>*>(to) = o;
+  } else {
+#pragma unroll
+    for (int j = 0; j < Elem<T>::V; ++j) to[j] = o.v[j];
+  }
+}
+
+// Pass 2: the gradient of packs tid, tid + THREADS, ... to out; after as above
+template <typename T, int THREADS, bool ALIGNED, typename F>
+__device__ __forceinline__ void emit_grad(const Softmax<T>& x, float ws, const Pack<T>* packs, int nv, int tid, T* out,
+                                          F after) {
+  constexpr int VL = Elem<T>::V;
+  int i = tid;
+  for (; i + (kAhead - 1) * THREADS < nv; i += kAhead * THREADS) {
+    Pack<T> p[kAhead];
+    const Pack<T>* from = packs + i;
+    T* to = out + (int64_t)i * VL;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) p[a] = from[a * THREADS];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      Pack<T> o;
+      x.pack(p[a], ws, o);
+      store_pack<T, ALIGNED>(o, to + a * THREADS * VL);
+    }
+    after(i, kAhead);
+  }
+  for (; i < nv; i += THREADS) {
+    Pack<T> o;
+    x.pack(packs[i], ws, o);
+    store_pack<T, ALIGNED>(o, out + (int64_t)i * VL);
+    after(i, 1);
+  }
+}
+
+// A far row's sum, from its maximum: (z - all) c cannot overflow upwards
+template <typename T, int WARPS, typename F>
+__device__ __forceinline__ float far_sum(const T* z, int64_t V, int tid, float all, float c, float2* buf, F barrier) {
+  float s = 0.f;
+  for (int64_t v = tid; v < V; v += WARPS * 32) s += ex2((Elem<T>::up(z[v]) - all) * c);
+  s = warp_sum(s);
+  if (WARPS > 1) {
+    barrier();                      // buf has been read
+    if ((tid & 31) == 0) buf[tid >> 5].y = s;
+    barrier();
+    s = warp_sum((tid & 31) < WARPS ? buf[tid & 31].y : 0.f);
+  }
+  return s;
+}
 
 // The teacher's entries of a row in shared memory, K of each.
 struct Entries {
@@ -228,28 +287,45 @@ __device__ __forceinline__ bool read_teacher(const Teacher& te, int r, const T* 
 }
 
 // one warp: T^2 * sum of q (log q - log p); lane 0 has it
-__device__ __forceinline__ float row_loss_of(const Entries& e, int K, float all, float log2_s, float inv_T, float T) {
-  const float log_s = log2_s * 0.6931471805599453f;
+template <typename T>
+__device__ __forceinline__ float row_loss_of(const Entries& e, int K, const Softmax<T>& x, float temperature) {
+  const float log2_s = log2f(x.s);
   float loss = 0.f;
   for (int k = threadIdx.x & 31; k < K; k += 32)
-    if (e.id[k] >= 0 && !(e.q[k] == 0.f)) loss += e.q[k] * (e.lq[k] - ((e.zk[k] - all) * inv_T - log_s));
-  return warp_sum(loss) * (T * T);
+    if (e.id[k] >= 0 && !(e.q[k] == 0.f))
+      loss += e.q[k] * (e.lq[k] - (x.log2_e(e.zk[k]) - log2_s) * 0.6931471805599453f);
+  return warp_sum(loss) * (temperature * temperature);
 }
 
-// thread tid of THREADS: the gradient at the teacher's entries.  The first of
-// the entries with the same index writes for all of them.
+// one warp: whether two of a row's entries may have the same index (K entries
+// against those before them; more than 128 are taken to)
+__device__ __forceinline__ bool repeated(const Entries& e, int K) {
+  if (K > 128) return true;
+  bool twice = false;
+  for (int k = threadIdx.x & 31; k < K; k += 32)
+    for (int i = 0; i < k; ++i) twice |= e.id[i] == e.id[k] && e.id[k] >= 0;
+  return __any_sync(0xffffffffu, twice);
+}
+
+// thread tid of `threads`: the gradient at the teacher's entries, w (p - q).
+// Where an index may be there twice, the first of its entries writes for all.
 template <typename T>
-__device__ __forceinline__ void correct(const Entries& e, int K, int tid, int threads, const Gradient<T>& g, T* dz) {
+__device__ __forceinline__ void correct(const Entries& e, int K, bool twice, int tid, int threads, const Softmax<T>& x,
+                                        float w, T* dz) {
+  const float inv_s = 1.f / x.s;
   for (int k = tid; k < K; k += threads) {
     if (e.id[k] < 0) continue;
     bool mine = true;
-    float sum = 0.f;
-    for (int i = 0; i < K; ++i)
-      if (e.id[i] == e.id[k]) {
-        if (i < k) mine = false;
-        sum += e.q[i];
-      }
-    if (mine) dz[e.id[k]] = Elem<T>::down(g.w * (g.p(e.zk[k]) - sum));
+    float sum = e.q[k];
+    if (twice) {
+      sum = 0.f;
+      for (int i = 0; i < K; ++i)
+        if (e.id[i] == e.id[k]) {
+          if (i < k) mine = false;
+          sum += e.q[i];
+        }
+    }
+    if (mine) dz[e.id[k]] = Elem<T>::down(w * (ex2(x.log2_e(e.zk[k])) * inv_s - sum));
   }
 }
 
@@ -268,15 +344,14 @@ __device__ __forceinline__ void zero_row(T* dz, int64_t V, int tid, int threads)
 // a warp (short rows, four a block).  The row is read twice, for the maximum
 // and sum of the softmax and for the gradient (the second time from L2).
 template <typename T, int ROW_THREADS>
-__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THREADS == 32 ? 8 : 2)
+__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THREADS == 32 ? 6 : 3)
     k_distill_rows(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, float temperature,
                    float gscale, int* count, int count_here, float* __restrict__ row_loss, T* dZ, int64_t ldd,
                    int* status) {
-  constexpr int VL = Elem<T>::V;
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
   extern __shared__ float entries[];              // per row: 4 arrays of K
   __shared__ float2 buf[WARPS];
-  __shared__ int some[ROWS];
+  __shared__ int some[ROWS];                      // 0: no entry counts; 1; 2: an index may be there twice
   griddep_wait();
   griddep_launch();
   const int tid = threadIdx.x % ROW_THREADS, in_block = threadIdx.x / ROW_THREADS;
@@ -292,8 +367,9 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THR
   const RowView<T> v(Z + (int64_t)r * ldz, V);
   if (tid < 32) {
     const bool any = read_teacher(te, r, v.z, V, inv_T, e, status);
+    const bool twice = any && dZ != nullptr && repeated(e, te.K);
     if (tid == 0) {
-      some[in_block] = any;
+      some[in_block] = any + twice;
       if (any && count_here) atomicAdd(&count[m], 1);
       if (!any) row_loss[r] = 0.f;
     }
@@ -305,34 +381,29 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THR
     return;
   }
   Running run;
-  absorb<T, ROW_THREADS>(run, v.packs(), v.nv, tid, c, [](int) {});
+  absorb<T, ROW_THREADS>(run, v.packs(), v.nv, tid, c, [](int, int) {});
   if (tid < v.head) run.one(Elem<T>::up(v.z[tid]), c);
   if (tid < v.n_tail) run.one(Elem<T>::up(v.z[v.tail + tid]), c);
   float all, s;
   join_row<WARPS>(run, tid, c, buf, sync, all, s);
-  const float log2_s = log2f(s);
+  Softmax<T> x(all, s, c);
+  if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf, sync);
   if (tid < 32) {
-    const float loss = row_loss_of(e, te.K, all, log2_s, inv_T, temperature);
+    const float loss = row_loss_of(e, te.K, x, temperature);
     if (tid == 0) row_loss[r] = loss;
   }
   if (dz == nullptr) return;
-  const Gradient<T> g{all, c, log2_s, gscale * temperature / (float)count[m]};
-  const bool aligned = RowView<T>(dz, V).mis == v.mis;
-  const Pack<T>* packs = v.packs();
-  T* out = dz + v.head;
-  int i = tid;
-  for (; i + (kAhead - 1) * ROW_THREADS < v.nv; i += kAhead * ROW_THREADS) {
-    Pack<T> p[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * ROW_THREADS];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) g.pack(p[a], out + (int64_t)(i + a * ROW_THREADS) * VL, aligned);
+  const float w = gscale * temperature / (float)count[m], ws = w / x.s;
+  if (x.far) {
+    for (int64_t i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+  } else {
+    if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, ROW_THREADS, true>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
+    else emit_grad<T, ROW_THREADS, false>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
+    if (tid < v.head) dz[tid] = x.grad(Elem<T>::up(v.z[tid]), w);
+    if (tid < v.n_tail) dz[v.tail + tid] = x.grad(Elem<T>::up(v.z[v.tail + tid]), w);
   }
-  for (; i < v.nv; i += ROW_THREADS) g.pack(packs[i], out + (int64_t)i * VL, aligned);
-  if (tid < v.head) dz[tid] = g.one(Elem<T>::up(v.z[tid]));
-  if (tid < v.n_tail) dz[v.tail + tid] = g.one(Elem<T>::up(v.z[v.tail + tid]));
   sync();
-  correct(e, te.K, tid, ROW_THREADS, g, dz);
+  correct(e, te.K, some[in_block] == 2, tid, ROW_THREADS, x, w, dz);
 }
 
 // A block stays and takes row after row, each in shared memory: the next row
@@ -345,10 +416,10 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
     k_distill_resident(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, int slots,
                        float temperature, float gscale, int* count, int count_here, float* __restrict__ row_loss,
                        T* dZ, int64_t ldd, int* status) {
-  constexpr int VL = Elem<T>::V, WARPS = THREADS / 32;
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ uint4 row_at[];               // `slots` packs, then twice 4 arrays of K
   __shared__ float2 buf[2][WARPS];
-  __shared__ int some[2];
+  __shared__ int some[2];                         // as above
   griddep_wait();
   griddep_launch();
   float* entries = reinterpret_cast<float*>(row_at + slots);
@@ -356,41 +427,56 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
   const int tid = threadIdx.x;
   const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
   const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row_at);
+  auto all_warps = [] { __syncthreads(); };
   int b = 0;
   if (tid >= THREADS) {                           // the teacher's warp
+    const int lane = tid & 31;
     auto prepare = [&](int r, int to) {
-      const bool any = read_teacher(te, r, Z + (int64_t)r * ldz, V, inv_T, Entries(entries + to * 4 * te.K, te.K), status);
-      if ((tid & 31) == 0) {
-        some[to] = any;
+      const Entries e(entries + to * 4 * te.K, te.K);
+      const bool any = read_teacher(te, r, Z + (int64_t)r * ldz, V, inv_T, e, status);
+      const bool twice = any && dZ != nullptr && repeated(e, te.K);
+      if (lane == 0) {
+        some[to] = any + twice;
         if (any && count_here) atomicAdd(&count[worker_of(map.start, map.M, r)], 1);
       }
     };
     prepare(blockIdx.x, 0);
     for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
       __syncthreads();                            // the row's maxima and sums are in buf
-      const Entries e(entries + b * 4 * te.K, te.K);
-      const bool any = some[b] != 0;
-      const float2 x = (tid & 31) < WARPS ? buf[b][tid & 31] : make_float2(-INFINITY, 0.f);
-      const float all = warp_max(x.x);
-      const float s = warp_sum(x.x == -INFINITY ? x.y : x.y * ex2((x.x - all) * c));
-      const float loss = any ? row_loss_of(e, te.K, all, log2f(s), inv_T, temperature) : 0.f;
-      if ((tid & 31) == 0) row_loss[r] = loss;
+      float2 t = lane < WARPS ? buf[b][lane] : make_float2(-INFINITY, 0.f);
+      join_lanes(c, t.x, t.y);
+      Softmax<T> x(t.x, t.y, c);
+      if (x.far) {                                // as in far_sum
+        __syncthreads();
+        __syncthreads();
+        x.s = warp_sum(lane < WARPS ? buf[b][lane].y : 0.f);
+      }
+      const float loss = some[b] ? row_loss_of(Entries(entries + b * 4 * te.K, te.K), te.K, x, temperature) : 0.f;
+      if (lane == 0) row_loss[r] = loss;
       if (r + (int64_t)gridDim.x < N) prepare(r + gridDim.x, b ^ 1);
     }
     return;
   }
-  auto fetch = [&](const RowView<T>& v, int i) {
-    if (i < v.nv) copy16(&row_at[i], v.packs() + i, true);
+  unsigned slot = (unsigned)__cvta_generic_to_shared(row_at);
+  // packs i, i + THREADS, ..., n of them, of the next row
+  auto fetch = [&](const Pack<T>* from, int nv, int i, int n) {
+    from += i;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (a < n && i + a * THREADS < nv)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (i + a * THREADS) * 16), "l"(from + a * THREADS)
+                     : "memory");
   };
   {
     const RowView<T> v(Z + (int64_t)blockIdx.x * ldz, V);
-    for (int i = tid; i < v.nv; i += THREADS) fetch(v, i);
+    for (int i = tid; i < v.nv; i += THREADS) fetch(v.packs(), v.nv, i, 1);
   }
   for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
     const RowView<T> v(Z + (int64_t)r * ldz, V);
     const bool more = r + (int64_t)gridDim.x < N;
-    RowView<T> next(Z + (int64_t)(more ? r + gridDim.x : r) * ldz, V);
-    if (!more) next.nv = 0;
+    const RowView<T> next(Z + (int64_t)(more ? r + gridDim.x : r) * ldz, V);
+    const Pack<T>* next_packs = next.packs();
+    const int next_nv = more ? next.nv : 0;
     const float edge0 = tid < v.head ? Elem<T>::up(v.z[tid]) : -INFINITY;
     const float edge1 = tid < v.n_tail ? Elem<T>::up(v.z[v.tail + tid]) : -INFINITY;
     const float n = dZ != nullptr ? (float)count[worker_of(map.start, map.M, r)] : 1.f;
@@ -398,46 +484,39 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
     copy_wait<0>();
     Running run;
     if (dZ != nullptr) {
-      absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int) {});
+      absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int, int) {});
     } else {
-      absorb<T, THREADS>(run, packs, v.nv, tid, c, [&](int i) { fetch(next, i); });
+      absorb<T, THREADS>(run, packs, v.nv, tid, c, [&](int i, int k) { fetch(next_packs, next_nv, i, k); });
     }
     if (tid < v.head) run.one(edge0, c);
     if (tid < v.n_tail) run.one(edge1, c);
     float all, s;
-    join_row<WARPS>(run, tid, c, buf[b], [] { __syncthreads(); }, all, s);
-    int i = tid;
+    join_row<WARPS>(run, tid, c, buf[b], all_warps, all, s);
+    Softmax<T> x(all, s, c);
+    if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf[b], all_warps);
+    int done = tid;                               // the first pack of this thread's that is not yet copied
+    while (done < v.nv) done += THREADS;
     if (dZ != nullptr) {
       T* dz = dZ + (int64_t)r * ldd;
-      const Gradient<T> g{all, c, log2f(s), gscale * temperature / n};
-      if (some[b]) {
-        const bool aligned = RowView<T>(dz, V).mis == v.mis;
-        T* out = dz + v.head;
-        for (; i + (kAhead - 1) * THREADS < v.nv; i += kAhead * THREADS) {
-          Pack<T> p[kAhead];
-#pragma unroll
-          for (int a = 0; a < kAhead; ++a) p[a] = packs[i + a * THREADS];
-#pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            g.pack(p[a], out + (int64_t)(i + a * THREADS) * VL, aligned);
-            fetch(next, i + a * THREADS);
-          }
-        }
-        for (; i < v.nv; i += THREADS) {
-          g.pack(packs[i], out + (int64_t)i * VL, aligned);
-          fetch(next, i);
-        }
-        if (tid < v.head) dz[tid] = g.one(edge0);
-        if (tid < v.n_tail) dz[v.tail + tid] = g.one(edge1);
+      const int kind = some[b];
+      const float w = gscale * temperature / n, ws = w / x.s;
+      auto after = [&](int i, int k) { fetch(next_packs, next_nv, i, k); };
+      if (kind == 0 || x.far) {
+        if (kind == 0) zero_row(dz, V, tid, THREADS);
+        else
+          for (int64_t i = tid; i < V; i += THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+        done = tid;
       } else {
-        zero_row(dz, V, tid, THREADS);
+        if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, THREADS, true>(x, ws, packs, v.nv, tid, dz + v.head, after);
+        else emit_grad<T, THREADS, false>(x, ws, packs, v.nv, tid, dz + v.head, after);
+        if (tid < v.head) dz[tid] = x.grad(edge0, w);
+        if (tid < v.n_tail) dz[v.tail + tid] = x.grad(edge1, w);
       }
-      for (; i < next.nv; i += THREADS) fetch(next, i);   // packs that this row has not
+      for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
       asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");  // the row's gradient is written
-      if (some[b]) correct(Entries(entries + b * 4 * te.K, te.K), te.K, tid, THREADS, g, dz);
+      if (kind) correct(Entries(entries + b * 4 * te.K, te.K), te.K, kind == 2, tid, THREADS, x, w, dz);
     } else {
-      while (i < v.nv) i += THREADS;
-      for (; i < next.nv; i += THREADS) fetch(next, i);
+      for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
     }
   }
 }
@@ -498,15 +577,16 @@ void run_resident(cudaStream_t s, const DistillArgs& a, const RowMap& map, const
 // A warp for the shortest rows, so that most of it has something to load; rows
 // of which two fit an SM's shared memory stay there; longer ones are read twice.
 constexpr size_t kResidentBytes = 112 * 1024;
+constexpr int kLong = 256;
 template <typename T>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
   const int64_t fixed = (int64_t)2 * 4 * a.K * 4 + 512;
   if (a.V <= 1024) run_rows<T, 32>(s, a, map, te);
   else if (a.V <= 8192) run_resident<T, 128>(s, a, map, te);
-  else if (a.V * (int64_t)sizeof(T) + 16 * 512 + fixed <= (int64_t)kResidentBytes &&
-           (int64_t)resident_slots(a, sizeof(T), 512) * 16 + fixed <= (int64_t)kResidentBytes)
-    run_resident<T, 512>(s, a, map, te);
-  else run_rows<T, 512>(s, a, map, te);
+  else if (a.V * (int64_t)sizeof(T) + 16 * kLong + fixed <= (int64_t)kResidentBytes &&
+           (int64_t)resident_slots(a, sizeof(T), kLong) * 16 + fixed <= (int64_t)kResidentBytes)
+    run_resident<T, kLong>(s, a, map, te);
+  else run_rows<T, 256>(s, a, map, te);
 }
 
 }  // namespace

@@ -444,6 +444,42 @@ def test_distill_entry_on_a_masked_logit_and_nonfinite_rows():
     assert torch.isfinite(row_loss[4]) and torch.isfinite(dZ[4]).all() and int(count[0]) == 5
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [40, 3000, 20003, 140001])
+def test_distill_rows_of_the_types_extreme_values(dt, V):
+    """Rows masked with the type's lowest value, wholly and all but a few, rows
+    at its largest value, and rows far from zero."""
+    opt = handle([(1, 4)], 1, 6, 4)
+    f = torch.finfo(DT[dt])
+    Z = torch.randn(6, V, generator=gen(V), device="cuda").to(DT[dt])
+    Z[0] = f.min                      # all masked: p = 1 / V
+    Z[1] = f.min
+    Z[1, 5:9] = 1.5                   # p = 1 / 4 there
+    Z[2] = f.max
+    Z[3] = f.min
+    Z[3, 7] = f.max                   # p = 1 there
+    Z[4] += 900
+    Z[5] -= 900
+    idx = torch.tensor([[7, 5]] * 6, dtype=torch.int32, device="cuda")
+    t = torch.zeros(6, 2, device="cuda")
+    _, count, row_loss, dZ = run_distill(opt, Z, idx, t, [6], 1.0, 1.0)
+    z = Z.double()
+    p = torch.softmax(z - z.amax(1, keepdim=True), 1)
+    want = p.clone()
+    want[:, 7] -= 0.5
+    want[:, 5] -= 0.5
+    a = (z.amax(1, keepdim=True) - z).clamp(max=200)
+    tol = (p * U * (5 * ref.depth(V) + 20 + 10 * a) + 4 * U * want.abs()) / 6
+    ref.assert_within(dZ, f64(want / 6), f64(tol + ref.half(DT[dt]) * (want.abs() / 6 + tol)) + ref.tiny(DT[dt]), "dZ")
+    lp = torch.log_softmax(z - z.amax(1, keepdim=True), 1)
+    loss = -0.5 * (lp[:, 7] + lp[:, 5]) - np.log(2.0)
+    fine = [0, 1, 2, 4, 5]
+    ref.assert_within(row_loss[fine], f64(loss)[fine], f64(U * (5 * ref.depth(V) + 40 + 10 * loss.abs()))[fine], "row_loss")
+    # the teacher's second entry sits where p = 0: as far below as the type goes
+    gap = 0.5 * (float(f.max) - float(f.min))
+    assert float(row_loss[3]) > 0.49 * min(gap * 2, 3e38)
+
+
 def test_distill_reports_an_index_beyond_the_row():
     opt = handle([(1, 4)], 1, 2, 4)
     Z = torch.randn(2, 9, generator=gen(31), device="cuda")
