@@ -347,6 +347,7 @@ struct DistillArgs {
   void* dZ;
   int64_t ldd;
   int* count;                  // workspace: M counters, zero between calls
+  void* scratch;               // workspace: 12 bytes per row
   int* status;
 };
 void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int M);

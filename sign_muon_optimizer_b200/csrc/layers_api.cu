@@ -109,7 +109,8 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 int norm_blocks(signmuon_t h) { return h->n_sm * 8 + h->M; }
 
 // workspace layout, in bytes: embed_grad has two key arrays, digit counts and
-// the parts of cut runs, layernorm_grad the blocks' sums, distill the rows' losses
+// the parts of cut runs, layernorm_grad the blocks' sums, distill the
+// rows' losses and stats
 int64_t embed_units(signmuon_t h, int64_t rows) {
   const int64_t most = (sm::kFewBlocks + 1) * 256;   // rows that may go in units of 64
   const int64_t a = (rows < most ? rows : most) / 64, b = rows / 256;
@@ -139,7 +140,7 @@ int signmuon_layers_reserve(signmuon_t h, int64_t max_rows, int64_t max_cols) {
     int64_t n = embed_bytes(h, max_rows, max_cols);
     const int64_t b = norm_bytes(h, max_cols < SIGNMUON_LAYERNORM_MAX_COLS ? max_cols : SIGNMUON_LAYERNORM_MAX_COLS);
     if (b > n) n = b;
-    if (max_rows * 4 > n) n = max_rows * 4;
+    if (max_rows * 16 > n) n = max_rows * 16;   // distill: the rows' losses, and 12 bytes of scratch
     uint8_t* ws = nullptr;
     TRY(dalloc(h, &ws, n));
     if (h->lay_status == nullptr) {
@@ -364,6 +365,7 @@ int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t
     a.dZ = n > 0 ? dZ : nullptr;
     a.ldd = ldd;
     a.count = h->lay_status + 1;
+    a.scratch = h->lay_ws + h->lay_rows * 4;
     a.status = h->lay_status;
     NvtxRange range("signmuon distill");
     sm::launch_distill(h->stream, a, start, h->M);

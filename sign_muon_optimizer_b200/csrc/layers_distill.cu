@@ -25,25 +25,85 @@ struct Teacher {
   int K;
 };
 
-// count[m] += rows of worker m with an entry that counts: a warp per row, one
-// addition per block and worker
-__global__ void __launch_bounds__(1024) k_distill_count(const RowMap map, const Teacher te, int64_t V, int* count) {
-  __shared__ int any_of[32];
+// What a row's entries come to: nothing to learn from, or the softmax of the
+// teacher's logits, exp((t - top) / T - log_sum), and whether an index is there
+// twice.
+struct RowStat {
+  float top, log_sum;
+};
+enum RowKind { ROW_NONE = 0, ROW_ONCE = 1, ROW_TWICE = 2 };
+
+// The rows' stats and kinds, and count[m] += worker m's rows of a kind other
+// than none.  A row takes G threads: a warp (K <= 128), or the block.  Repeated
+// indices are found by inserting all of them into a hash table of 2 K slots.
+template <int G>
+__global__ void __launch_bounds__(256) k_distill_teacher(const RowMap map, const Teacher te, int64_t V, float inv_T,
+                                                         RowStat* __restrict__ stat, int* __restrict__ kind, int* count,
+                                                         int* status) {
+  constexpr int ROWS = 256 / G, SLOTS = G == 32 ? 256 : 2048;
+  __shared__ int table[ROWS][SLOTS];
+  __shared__ float part[8];
+  __shared__ int any_of[ROWS];
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t r = (int64_t)blockIdx.x * 32 + w;
-  bool any = false;
-  if (r < map.start[map.M])
-    for (int k = lane; k < te.K; k += 32)
-      any |= counts(load_id(te.idx, te.id64, r * te.ldt + k), V, load_t(te.t, te.t_type, r * te.ldt + k));
-  any = __any_sync(0xffffffffu, any);
-  if (lane == 0) any_of[w] = any;
+  const int in_block = threadIdx.x / G, tid = threadIdx.x % G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int N = map.start[map.M];
+  const int64_t r = (int64_t)blockIdx.x * ROWS + in_block;
+  const int K = r < N ? te.K : 0;
+  auto sync = [&] {
+    if (G == 32) __syncwarp();
+    else __syncthreads();
+  };
+  auto over_row = [&](float v, bool maximum) {    // sum or maximum over the row's threads
+    v = maximum ? warp_max(v) : warp_sum(v);
+    if (G == 32) return v;
+    __syncthreads();
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    v = part[0];
+    for (int i = 1; i < 8; ++i) v = maximum ? fmaxf(v, part[i]) : v + part[i];
+    return v;
+  };
+  for (int i = tid; i < SLOTS; i += G) table[in_block][i] = -1;
+  sync();
+  float top = -INFINITY;
+  bool any = false, twice = false;
+  for (int k = tid; k < K; k += G) {
+    const int64_t i = load_id(te.idx, te.id64, r * te.ldt + k);
+    const float t = load_t(te.t, te.t_type, r * te.ldt + k);
+    if (i >= V) *status = 1;
+    if (!counts(i, V, t)) continue;
+    any = true;
+    top = fmaxf(top, t);
+    unsigned at = ((unsigned)i * 2654435761u) >> 16;
+    for (int probes = 0; probes < SLOTS; ++probes, ++at) {
+      const int old = atomicCAS(&table[in_block][at % SLOTS], -1, (int)i);
+      if (old == (int)i) twice = true;
+      if (old == -1 || old == (int)i) break;
+    }
+  }
+  any = over_row(any ? 1.f : 0.f, true) != 0.f;
+  twice = over_row(twice ? 1.f : 0.f, true) != 0.f;
+  top = over_row(top, true);
+  float sum = 0.f;
+  for (int k = tid; k < K; k += G) {
+    const int64_t i = load_id(te.idx, te.id64, r * te.ldt + k);
+    const float t = load_t(te.t, te.t_type, r * te.ldt + k);
+    if (counts(i, V, t)) sum += expf((t - top) * inv_T);
+  }
+  sum = over_row(sum, false);
+  if (tid == 0) {
+    any_of[in_block] = any;
+    if (r < N) {
+      stat[r] = RowStat{top, logf(sum)};
+      kind[r] = any ? (twice ? ROW_TWICE : ROW_ONCE) : ROW_NONE;
+    }
+  }
   __syncthreads();
-  if (w != 0) return;
+  if (warp != 0) return;
   // lane i: row i of the block
-  const int64_t mine = (int64_t)blockIdx.x * 32 + lane;
-  const int m = any_of[lane] ? worker_of(map.start, map.M, (int)mine) : -1;
+  const int m = lane < ROWS && any_of[lane < ROWS ? lane : 0]
+                    ? worker_of(map.start, map.M, (int)((int64_t)blockIdx.x * ROWS + lane)) : -1;
   const unsigned same = __match_any_sync(0xffffffffu, m);
   if (m >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[m], __popc(same));
 }
@@ -242,91 +302,59 @@ __device__ __forceinline__ float far_sum(const T* z, int64_t V, int tid, float a
   return s;
 }
 
-// The teacher's entries of a row in shared memory, K of each.
+// A row's entries in shared memory, K of each: index (-1: absent), probability
+// and the student's logit there.
 struct Entries {
-  float *q, *lq, *zk;   // probability, its logarithm, the student's logit there
-  int* id;              // -1: absent
-  __device__ __forceinline__ Entries(float* at, int K)
-      : q(at), lq(at + K), zk(at + 2 * K), id(reinterpret_cast<int*>(at + 3 * K)) {}
+  int* id;
+  float *q, *zk;
+  __device__ __forceinline__ Entries(float* at, int K) : id(reinterpret_cast<int*>(at)), q(at + K), zk(at + 2 * K) {}
 };
 
-// one warp: row r's entries; true if one counts
-template <typename T>
-__device__ __forceinline__ bool read_teacher(const Teacher& te, int r, const T* z, int64_t V, float inv_T,
-                                             const Entries& e, int* status) {
-  const int lane = threadIdx.x & 31;
-  float top = -INFINITY;
-  bool any = false;
-  for (int k = lane; k < te.K; k += 32) {
-    const int64_t i = load_id(te.idx, te.id64, (int64_t)r * te.ldt + k);
-    const float t = load_t(te.t, te.t_type, (int64_t)r * te.ldt + k);
-    if (i >= V) *status = 1;
-    const bool c = counts(i, V, t);
-    any |= c;
-    e.id[k] = c ? (int)i : -1;
-    e.lq[k] = t;
-    if (c) {
-      top = fmaxf(top, t);
-      e.zk[k] = Elem<T>::up(z[i]);
-    }
-  }
-  if (!__any_sync(0xffffffffu, any)) return false;
-  top = warp_max(top);
-  float sum = 0.f;
-  for (int k = lane; k < te.K; k += 32)
-    if (e.id[k] >= 0) sum += expf((e.lq[k] - top) * inv_T);
-  const float log_sum = logf(warp_sum(sum));
-  for (int k = lane; k < te.K; k += 32) {
-    if (e.id[k] < 0) continue;
-    const float lq = (e.lq[k] - top) * inv_T - log_sum;
-    e.lq[k] = lq;
-    e.q[k] = expf(lq);
-  }
-  __syncwarp();
-  return true;
+// an entry as it is read: its index, or -1, and its logit
+struct Entry {
+  int id;
+  float t;
+};
+__device__ __forceinline__ Entry load_entry(const Teacher& te, int r, int k, int64_t V) {
+  const int64_t i = load_id(te.idx, te.id64, (int64_t)r * te.ldt + k);
+  const float t = load_t(te.t, te.t_type, (int64_t)r * te.ldt + k);
+  return Entry{counts(i, V, t) ? (int)i : -1, t};
 }
 
-// one warp: T^2 * sum of q (log q - log p); lane 0 has it
-template <typename T>
-__device__ __forceinline__ float row_loss_of(const Entries& e, int K, const Softmax<T>& x, float temperature) {
-  const float log2_s = log2f(x.s);
-  float loss = 0.f;
-  for (int k = threadIdx.x & 31; k < K; k += 32)
-    if (e.id[k] >= 0 && !(e.q[k] == 0.f))
-      loss += e.q[k] * (e.lq[k] - (x.log2_e(e.zk[k]) - log2_s) * 0.6931471805599453f);
-  return warp_sum(loss) * (temperature * temperature);
+// Entry k into shared memory; returns its part q log q of the loss.
+__device__ __forceinline__ float put_entry(const Entries& e, int k, const Entry& x, float zk, const RowStat& st, float inv_T) {
+  const float lq = (x.t - st.top) * inv_T - st.log_sum;
+  const float q = x.id >= 0 ? expf(lq) : 0.f;
+  e.id[k] = x.id;
+  e.q[k] = q;
+  e.zk[k] = zk;
+  return q == 0.f ? 0.f : q * lq;
 }
 
-// one warp: whether two of a row's entries may have the same index (K entries
-// against those before them; more than 128 are taken to)
-__device__ __forceinline__ bool repeated(const Entries& e, int K) {
-  if (K > 128) return true;
-  bool twice = false;
-  for (int k = threadIdx.x & 31; k < K; k += 32)
-    for (int i = 0; i < k; ++i) twice |= e.id[i] == e.id[k] && e.id[k] >= 0;
-  return __any_sync(0xffffffffu, twice);
+// entry k's part -q log p of the loss (q = 0: nothing, whatever p is)
+template <typename T>
+__device__ __forceinline__ float cross(const Entries& e, int k, const Softmax<T>& x, float log2_s) {
+  const float q = e.q[k];
+  return q == 0.f ? 0.f : q * ((log2_s - x.log2_e(e.zk[k])) * 0.6931471805599453f);
 }
 
-// thread tid of `threads`: the gradient at the teacher's entries, w (p - q).
-// Where an index may be there twice, the first of its entries writes for all.
+// The gradient at entry k, w (p - q).  Where an index may be there twice, the
+// first of its entries writes for all.
 template <typename T>
-__device__ __forceinline__ void correct(const Entries& e, int K, bool twice, int tid, int threads, const Softmax<T>& x,
-                                        float w, T* dz) {
-  const float inv_s = 1.f / x.s;
-  for (int k = tid; k < K; k += threads) {
-    if (e.id[k] < 0) continue;
-    bool mine = true;
-    float sum = e.q[k];
-    if (twice) {
-      sum = 0.f;
-      for (int i = 0; i < K; ++i)
-        if (e.id[i] == e.id[k]) {
-          if (i < k) mine = false;
-          sum += e.q[i];
-        }
-    }
-    if (mine) dz[e.id[k]] = Elem<T>::down(w * (ex2(x.log2_e(e.zk[k])) * inv_s - sum));
+__device__ __forceinline__ void correct(const Entries& e, int K, int k, bool twice, const Softmax<T>& x, float w, T* dz) {
+  const int id = e.id[k];
+  if (id < 0) return;
+  bool mine = true;
+  float sum = e.q[k];
+  if (twice) {
+    sum = 0.f;
+    for (int i = 0; i < K; ++i)
+      if (e.id[i] == id) {
+        if (i < k) mine = false;
+        sum += e.q[i];
+      }
   }
+  if (mine) dz[id] = Elem<T>::down(w * (ex2(x.log2_e(e.zk[k])) / x.s - sum));
 }
 
 template <typename T>
@@ -345,40 +373,39 @@ __device__ __forceinline__ void zero_row(T* dz, int64_t V, int tid, int threads)
 // and sum of the softmax and for the gradient (the second time from L2).
 template <typename T, int ROW_THREADS>
 __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THREADS == 32 ? 6 : 3)
-    k_distill_rows(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, float temperature,
-                   float gscale, int* count, int count_here, float* __restrict__ row_loss, T* dZ, int64_t ldd,
-                   int* status) {
+    k_distill_rows(const RowMap map, const Teacher te, const RowStat* __restrict__ stat, const int* __restrict__ kinds,
+                   const T* Z, int64_t ldz, int64_t V, float temperature, float gscale, const int* __restrict__ count,
+                   float* __restrict__ row_loss, T* dZ, int64_t ldd) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
-  extern __shared__ float entries[];              // per row: 4 arrays of K
+  extern __shared__ float entries[];              // per row: 3 arrays of K
   __shared__ float2 buf[WARPS];
-  __shared__ int some[ROWS];                      // 0: no entry counts; 1; 2: an index may be there twice
+  __shared__ float losses[WARPS];
   griddep_wait();
   griddep_launch();
   const int tid = threadIdx.x % ROW_THREADS, in_block = threadIdx.x / ROW_THREADS;
   const int r = blockIdx.x * ROWS + in_block;
   if (r >= map.start[map.M]) return;              // (a whole warp)
-  const Entries e(entries + (int64_t)in_block * 4 * te.K, te.K);
+  const Entries e(entries + (int64_t)in_block * 3 * te.K, te.K);
   auto sync = [&] {
     if (ROW_THREADS == 32) __syncwarp();
     else __syncthreads();
   };
-  const int m = worker_of(map.start, map.M, r);
   const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
   const RowView<T> v(Z + (int64_t)r * ldz, V);
-  if (tid < 32) {
-    const bool any = read_teacher(te, r, v.z, V, inv_T, e, status);
-    const bool twice = any && dZ != nullptr && repeated(e, te.K);
-    if (tid == 0) {
-      some[in_block] = any + twice;
-      if (any && count_here) atomicAdd(&count[m], 1);
-      if (!any) row_loss[r] = 0.f;
-    }
-  }
-  sync();
   T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
-  if (!some[in_block]) {
+  const int kind = kinds[r];
+  if (kind == ROW_NONE) {
     if (dz != nullptr) zero_row(dz, V, tid, ROW_THREADS);
+    if (tid == 0) row_loss[r] = 0.f;
     return;
+  }
+  float loss = 0.f;
+  {
+    const RowStat st = stat[r];
+    for (int k = tid; k < te.K; k += ROW_THREADS) {
+      const Entry x = load_entry(te, r, k, V);
+      loss += put_entry(e, k, x, x.id >= 0 ? Elem<T>::up(v.z[x.id]) : 0.f, st, inv_T);
+    }
   }
   Running run;
   absorb<T, ROW_THREADS>(run, v.packs(), v.nv, tid, c, [](int, int) {});
@@ -388,76 +415,57 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THR
   join_row<WARPS>(run, tid, c, buf, sync, all, s);
   Softmax<T> x(all, s, c);
   if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf, sync);
-  if (tid < 32) {
-    const float loss = row_loss_of(e, te.K, x, temperature);
-    if (tid == 0) row_loss[r] = loss;
-  }
-  if (dz == nullptr) return;
-  const float w = gscale * temperature / (float)count[m], ws = w / x.s;
-  if (x.far) {
-    for (int64_t i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+  const float log2_s = log2f(x.s);
+  for (int k = tid; k < te.K; k += ROW_THREADS) loss += cross(e, k, x, log2_s);
+  loss = warp_sum(loss);
+  if (WARPS > 1 && (tid & 31) == 0) losses[tid >> 5] = loss;
+  if (dz != nullptr) {
+    const float w = gscale * temperature / (float)count[worker_of(map.start, map.M, r)], ws = w / x.s;
+    if (x.far) {
+      for (int64_t i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+    } else {
+      if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, ROW_THREADS, true>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
+      else emit_grad<T, ROW_THREADS, false>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
+      if (tid < v.head) dz[tid] = x.grad(Elem<T>::up(v.z[tid]), w);
+      if (tid < v.n_tail) dz[v.tail + tid] = x.grad(Elem<T>::up(v.z[v.tail + tid]), w);
+    }
+    sync();
+    for (int k = tid; k < te.K; k += ROW_THREADS) correct(e, te.K, k, kind == ROW_TWICE, x, w, dz);
   } else {
-    if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, ROW_THREADS, true>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
-    else emit_grad<T, ROW_THREADS, false>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
-    if (tid < v.head) dz[tid] = x.grad(Elem<T>::up(v.z[tid]), w);
-    if (tid < v.n_tail) dz[v.tail + tid] = x.grad(Elem<T>::up(v.z[v.tail + tid]), w);
+    sync();
   }
-  sync();
-  correct(e, te.K, some[in_block] == 2, tid, ROW_THREADS, x, w, dz);
+  if (tid == 0) {
+    if (WARPS > 1) {
+      loss = 0.f;
+      for (int i = 0; i < WARPS; ++i) loss += losses[i];
+    }
+    row_loss[r] = loss * (temperature * temperature);
+  }
 }
 
 // A block stays and takes row after row, each in shared memory: the next row
 // comes in through asynchronous copies while this one's gradient goes out (or,
 // for the loss alone, while its sum is made), pack by pack into the places that
-// the same thread has just read.  One more warp works ahead on the teacher's
-// entries of the next row and does the loss.  Two blocks on an SM.
+// the same thread has just read.  The next row's entries are loaded a row ahead
+// too, the logits there at the row's start.  Two blocks on an SM.
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
-    k_distill_resident(const RowMap map, const Teacher te, const T* Z, int64_t ldz, int64_t V, int slots,
-                       float temperature, float gscale, int* count, int count_here, float* __restrict__ row_loss,
-                       T* dZ, int64_t ldd, int* status) {
+__global__ void __launch_bounds__(THREADS, THREADS > 128 ? 2 : 6)
+    k_distill_resident(const RowMap map, const Teacher te, const RowStat* __restrict__ stat,
+                       const int* __restrict__ kinds, const T* Z, int64_t ldz, int64_t V, int slots, float temperature,
+                       float gscale, const int* __restrict__ count, float* __restrict__ row_loss, T* dZ, int64_t ldd) {
   constexpr int WARPS = THREADS / 32;
-  extern __shared__ uint4 row_at[];               // `slots` packs, then twice 4 arrays of K
+  extern __shared__ uint4 row_at[];               // `slots` packs, then twice 3 arrays of K
   __shared__ float2 buf[2][WARPS];
-  __shared__ int some[2];                         // as above
+  __shared__ float losses[2][WARPS];
   griddep_wait();
   griddep_launch();
   float* entries = reinterpret_cast<float*>(row_at + slots);
-  const int N = map.start[map.M];
-  const int tid = threadIdx.x;
+  const int N = map.start[map.M], step = gridDim.x;
+  const int tid = threadIdx.x, K = te.K;
   const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
   const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row_at);
-  auto all_warps = [] { __syncthreads(); };
-  int b = 0;
-  if (tid >= THREADS) {                           // the teacher's warp
-    const int lane = tid & 31;
-    auto prepare = [&](int r, int to) {
-      const Entries e(entries + to * 4 * te.K, te.K);
-      const bool any = read_teacher(te, r, Z + (int64_t)r * ldz, V, inv_T, e, status);
-      const bool twice = any && dZ != nullptr && repeated(e, te.K);
-      if (lane == 0) {
-        some[to] = any + twice;
-        if (any && count_here) atomicAdd(&count[worker_of(map.start, map.M, r)], 1);
-      }
-    };
-    prepare(blockIdx.x, 0);
-    for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
-      __syncthreads();                            // the row's maxima and sums are in buf
-      float2 t = lane < WARPS ? buf[b][lane] : make_float2(-INFINITY, 0.f);
-      join_lanes(c, t.x, t.y);
-      Softmax<T> x(t.x, t.y, c);
-      if (x.far) {                                // as in far_sum
-        __syncthreads();
-        __syncthreads();
-        x.s = warp_sum(lane < WARPS ? buf[b][lane].y : 0.f);
-      }
-      const float loss = some[b] ? row_loss_of(Entries(entries + b * 4 * te.K, te.K), te.K, x, temperature) : 0.f;
-      if (lane == 0) row_loss[r] = loss;
-      if (r + (int64_t)gridDim.x < N) prepare(r + gridDim.x, b ^ 1);
-    }
-    return;
-  }
-  unsigned slot = (unsigned)__cvta_generic_to_shared(row_at);
+  auto sync = [] { __syncthreads(); };
+  const unsigned slot = (unsigned)__cvta_generic_to_shared(row_at);
   // packs i, i + THREADS, ..., n of them, of the next row
   auto fetch = [&](const Pack<T>* from, int nv, int i, int n) {
     from += i;
@@ -467,57 +475,96 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS > 128 ? 2 : 6)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (i + a * THREADS) * 16), "l"(from + a * THREADS)
                      : "memory");
   };
-  {
-    const RowView<T> v(Z + (int64_t)blockIdx.x * ldz, V);
+  auto finish_loss = [&](int r, int b) {          // thread 0, behind a barrier
+    float t = 0.f;
+    for (int i = 0; i < WARPS; ++i) t += losses[b][i];
+    row_loss[r] = t * (temperature * temperature);
+  };
+  int b = 0, r = blockIdx.x;
+  // this row's and the next one's kind; this row's first entry of the thread
+  int kind = kinds[r], kind1 = r + step < N ? kinds[r + step] : ROW_NONE;
+  Entry x0 = tid < K ? load_entry(te, r, tid, V) : Entry{-1, 0.f};
+  RowStat st = stat[r];
+  if (kind != ROW_NONE) {
+    const RowView<T> v(Z + (int64_t)r * ldz, V);
     for (int i = tid; i < v.nv; i += THREADS) fetch(v.packs(), v.nv, i, 1);
   }
-  for (int r = blockIdx.x; r < N; r += gridDim.x, b ^= 1) {
+  for (; r < N; r += step) {
     const RowView<T> v(Z + (int64_t)r * ldz, V);
-    const bool more = r + (int64_t)gridDim.x < N;
-    const RowView<T> next(Z + (int64_t)(more ? r + gridDim.x : r) * ldz, V);
-    const Pack<T>* next_packs = next.packs();
-    const int next_nv = more ? next.nv : 0;
+    const Entries e(entries + b * 3 * K, K);
+    // loads whose results are wanted later: the logits at the entries, the
+    // row's edges, the worker's count; the next row's first entries, the kind
+    // of the row behind it
+    const float zk = kind != ROW_NONE && x0.id >= 0 ? Elem<T>::up(v.z[x0.id]) : 0.f;
     const float edge0 = tid < v.head ? Elem<T>::up(v.z[tid]) : -INFINITY;
     const float edge1 = tid < v.n_tail ? Elem<T>::up(v.z[v.tail + tid]) : -INFINITY;
     const float n = dZ != nullptr ? (float)count[worker_of(map.start, map.M, r)] : 1.f;
-    copy_commit();
-    copy_wait<0>();
-    Running run;
-    if (dZ != nullptr) {
-      absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int, int) {});
-    } else {
-      absorb<T, THREADS>(run, packs, v.nv, tid, c, [&](int i, int k) { fetch(next_packs, next_nv, i, k); });
+    const int64_t r1 = (int64_t)r + step, r2 = r1 + step;
+    Entry x1{-1, 0.f};
+    RowStat st1 = st;
+    if (r1 < N) {
+      if (tid < K) x1 = load_entry(te, (int)r1, tid, V);
+      st1 = stat[r1];
     }
-    if (tid < v.head) run.one(edge0, c);
-    if (tid < v.n_tail) run.one(edge1, c);
-    float all, s;
-    join_row<WARPS>(run, tid, c, buf[b], all_warps, all, s);
-    Softmax<T> x(all, s, c);
-    if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf[b], all_warps);
-    int done = tid;                               // the first pack of this thread's that is not yet copied
-    while (done < v.nv) done += THREADS;
-    if (dZ != nullptr) {
-      T* dz = dZ + (int64_t)r * ldd;
-      const int kind = some[b];
-      const float w = gscale * temperature / n, ws = w / x.s;
-      auto after = [&](int i, int k) { fetch(next_packs, next_nv, i, k); };
-      if (kind == 0 || x.far) {
-        if (kind == 0) zero_row(dz, V, tid, THREADS);
-        else
-          for (int64_t i = tid; i < V; i += THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
-        done = tid;
-      } else {
-        if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, THREADS, true>(x, ws, packs, v.nv, tid, dz + v.head, after);
-        else emit_grad<T, THREADS, false>(x, ws, packs, v.nv, tid, dz + v.head, after);
-        if (tid < v.head) dz[tid] = x.grad(edge0, w);
-        if (tid < v.n_tail) dz[v.tail + tid] = x.grad(edge1, w);
+    const int kind2 = r2 < N ? kinds[r2] : ROW_NONE;
+    const RowView<T> next(Z + (r1 < N ? r1 : (int64_t)r) * ldz, V);
+    const Pack<T>* next_packs = next.packs();
+    const int next_nv = kind1 != ROW_NONE ? next.nv : 0;
+    auto after = [&](int i, int k) { fetch(next_packs, next_nv, i, k); };
+    T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
+    if (kind != ROW_NONE) {
+      copy_commit();
+      copy_wait<0>();
+      Running run;
+      if (dz != nullptr) absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int, int) {});
+      else absorb<T, THREADS>(run, packs, v.nv, tid, c, after);
+      if (tid < v.head) run.one(edge0, c);
+      if (tid < v.n_tail) run.one(edge1, c);
+      float loss = 0.f;
+      if (tid < K) loss = put_entry(e, tid, x0, zk, st, inv_T);
+      for (int k = tid + THREADS; k < K; k += THREADS) {
+        const Entry y = load_entry(te, r, k, V);
+        loss += put_entry(e, k, y, y.id >= 0 ? Elem<T>::up(v.z[y.id]) : 0.f, st, inv_T);
       }
-      for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
-      asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");  // the row's gradient is written
-      if (kind) correct(Entries(entries + b * 4 * te.K, te.K), te.K, kind == 2, tid, THREADS, x, w, dz);
+      float all, s;
+      join_row<WARPS>(run, tid, c, buf[b], sync, all, s);
+      Softmax<T> x(all, s, c);
+      if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf[b], sync);
+      const float log2_s = log2f(x.s);
+      for (int k = tid; k < K; k += THREADS) loss += cross(e, k, x, log2_s);
+      loss = warp_sum(loss);
+      if ((tid & 31) == 0) losses[b][tid >> 5] = loss;
+      int done = tid;                             // the first pack of this thread's that is not yet sent for
+      while (done < v.nv) done += THREADS;
+      if (dz != nullptr) {
+        const float w = gscale * temperature / n, ws = w / x.s;
+        if (x.far) {
+          for (int64_t i = tid; i < V; i += THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+          done = tid;
+        } else {
+          if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, THREADS, true>(x, ws, packs, v.nv, tid, dz + v.head, after);
+          else emit_grad<T, THREADS, false>(x, ws, packs, v.nv, tid, dz + v.head, after);
+          if (tid < v.head) dz[tid] = x.grad(edge0, w);
+          if (tid < v.n_tail) dz[v.tail + tid] = x.grad(edge1, w);
+        }
+        for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
+        __syncthreads();                          // the row's gradient is written
+        for (int k = tid; k < K; k += THREADS) correct(e, K, k, kind == ROW_TWICE, x, w, dz);
+      } else {
+        for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
+        __syncthreads();                          // the row's losses are in place
+      }
+      if (tid == 0) finish_loss(r, b);
+      b ^= 1;                                     // two barriers lie before these buffers are used again
     } else {
-      for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
+      if (dz != nullptr) zero_row(dz, V, tid, THREADS);
+      if (tid == 0) row_loss[r] = 0.f;
+      for (int i = tid; i < next_nv; i += THREADS) fetch(next_packs, next_nv, i, 1);
     }
+    kind = kind1;
+    kind1 = kind2;
+    x0 = x1;
+    st = st1;
   }
 }
 
@@ -544,16 +591,21 @@ __global__ void __launch_bounds__(256) k_distill_loss(const RowMap map, const fl
   }
 }
 
+struct Scratch {
+  RowStat* stat;
+  int* kind;
+};
+
 template <typename T, int ROW_THREADS>
-void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
+void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1;
-  const size_t smem = (size_t)ROWS * 4 * a.K * 4;
+  const size_t smem = (size_t)ROWS * 3 * a.K * 4;
   auto* kernel = k_distill_rows<T, ROW_THREADS>;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   count_launch();
   launch_pdl(kernel, dim3((map.start[map.M] + ROWS - 1) / ROWS), dim3(ROWS * ROW_THREADS), smem, s, map, te,
-             reinterpret_cast<const T*>(a.Z), a.ldz, a.V, a.temperature, a.gscale, a.count, a.dZ == nullptr ? 1 : 0,
-             a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd, a.status);
+             (const RowStat*)x.stat, (const int*)x.kind, reinterpret_cast<const T*>(a.Z), a.ldz, a.V, a.temperature,
+             a.gscale, (const int*)a.count, a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd);
 }
 
 int resident_slots(const DistillArgs& a, int elem, int threads) {
@@ -562,31 +614,29 @@ int resident_slots(const DistillArgs& a, int elem, int threads) {
 }
 
 template <typename T, int THREADS>
-void run_resident(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
+void run_resident(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   auto* kernel = k_distill_resident<T, THREADS>;
   const int slots = resident_slots(a, sizeof(T), THREADS);
-  const size_t smem = (size_t)slots * 16 + (size_t)2 * 4 * a.K * 4;
-  cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  const int grid = stream_grid((const void*)kernel, THREADS + 32, smem, map.start[map.M], 16);
+  const size_t smem = (size_t)slots * 16 + (size_t)2 * 3 * a.K * 4;
+  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int grid = stream_grid((const void*)kernel, THREADS, smem, map.start[map.M], 16);
   count_launch();
-  launch_pdl(kernel, dim3(grid), dim3(THREADS + 32), smem, s, map, te, reinterpret_cast<const T*>(a.Z), a.ldz, a.V,
-             slots, a.temperature, a.gscale, a.count, a.dZ == nullptr ? 1 : 0, a.row_loss, reinterpret_cast<T*>(a.dZ),
-             a.ldd, a.status);
+  launch_pdl(kernel, dim3(grid), dim3(THREADS), smem, s, map, te, (const RowStat*)x.stat, (const int*)x.kind,
+             reinterpret_cast<const T*>(a.Z), a.ldz, a.V, slots, a.temperature, a.gscale, (const int*)a.count,
+             a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd);
 }
 
 // A warp for the shortest rows, so that most of it has something to load; rows
 // of which two fit an SM's shared memory stay there; longer ones are read twice.
-constexpr size_t kResidentBytes = 112 * 1024;
+constexpr int64_t kResidentBytes = 112 * 1024;
 constexpr int kLong = 256;
 template <typename T>
-void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te) {
-  const int64_t fixed = (int64_t)2 * 4 * a.K * 4 + 512;
-  if (a.V <= 1024) run_rows<T, 32>(s, a, map, te);
-  else if (a.V <= 8192) run_resident<T, 128>(s, a, map, te);
-  else if (a.V * (int64_t)sizeof(T) + 16 * kLong + fixed <= (int64_t)kResidentBytes &&
-           (int64_t)resident_slots(a, sizeof(T), kLong) * 16 + fixed <= (int64_t)kResidentBytes)
-    run_resident<T, kLong>(s, a, map, te);
-  else run_rows<T, 256>(s, a, map, te);
+void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
+  const int64_t fixed = (int64_t)2 * 3 * a.K * 4 + 512;
+  if (a.V <= 1024) run_rows<T, 32>(s, a, map, te, x);
+  else if (a.V <= 8192) run_resident<T, 128>(s, a, map, te, x);
+  else if (a.V * (int64_t)sizeof(T) + 16 * kLong + fixed <= kResidentBytes) run_resident<T, kLong>(s, a, map, te, x);
+  else run_rows<T, kLong>(s, a, map, te, x);
 }
 
 }  // namespace
@@ -598,14 +648,18 @@ void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int 
   const int N = start[M];
   const Teacher te{a.idx, a.id64, a.t, a.t_type, a.ldt, a.K};
   if (N > 0) {
-    // the gradient needs the worker's row count before its first row is done
-    if (a.dZ != nullptr) {
-      count_launch();
-      launch_pdl(k_distill_count, dim3((unsigned)((N + 31LL) / 32)), dim3(1024), 0, s, map, te, a.V, a.count);
-    }
-    if (a.type == LT_F32) pick_rows<float>(s, a, map, te);
-    else if (a.type == LT_BF16) pick_rows<__nv_bfloat16>(s, a, map, te);
-    else pick_rows<__half>(s, a, map, te);
+    const Scratch x{reinterpret_cast<RowStat*>(a.scratch), reinterpret_cast<int*>(a.scratch) + 2 * (int64_t)N};
+    const float inv_T = 1.f / a.temperature;
+    count_launch();
+    if (a.K <= 128)
+      launch_pdl(k_distill_teacher<32>, dim3((unsigned)((N + 7LL) / 8)), dim3(256), 0, s, map, te, a.V, inv_T, x.stat,
+                 x.kind, a.count, a.status);
+    else
+      launch_pdl(k_distill_teacher<256>, dim3(N), dim3(256), 0, s, map, te, a.V, inv_T, x.stat, x.kind, a.count,
+                 a.status);
+    if (a.type == LT_F32) pick_rows<float>(s, a, map, te, x);
+    else if (a.type == LT_BF16) pick_rows<__nv_bfloat16>(s, a, map, te, x);
+    else pick_rows<__half>(s, a, map, te, x);
   }
   count_launch();
   launch_pdl(k_distill_loss, dim3(M), dim3(256), 0, s, map, (const float*)a.row_loss, a.count, a.loss, a.count_out);

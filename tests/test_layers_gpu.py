@@ -513,6 +513,29 @@ def test_distill_gradient_against_differences():
     assert abs(num - float((d * v).sum())) <= 1e-5 * float((np.abs(d) * np.abs(v)).sum()) + 1e-9
 
 
+@pytest.mark.parametrize("V", [300, 3000, 12000])
+@pytest.mark.parametrize("K", [1, 100, 300])
+@pytest.mark.parametrize("grad,in_place", [(True, False), (True, True), (False, False)])
+def test_distill_many_rows_with_gaps_and_repeats(V, K, grad, in_place):
+    """More rows than blocks, half of them without entries in runs of every
+    length, repeated indices in some."""
+    rows = [301, 0, 1500, 7]
+    n = sum(rows)
+    opt = handle([(1, 4)], len(rows), n, 4)
+    g = gen(V + K)
+    Z = (torch.randn(n, V, generator=g, device="cuda") * 2).to(torch.bfloat16)
+    idx, t = teacher(n, V, K, g, torch.int32, absent=0.3)
+    idx[::3, K // 2:] = idx[::3, :K - K // 2]          # the same index twice
+    gone = torch.rand(n // 4 + 1, generator=g, device="cuda").repeat_interleave(4)[:n] < 0.4
+    idx[gone] = -1
+    Zf, want = Z.double(), Z.clone()
+    got = run_distill(opt, Z, idx, t, rows, 2.0, 1.0, grad, in_place)
+    check_distill(got, f64(Zf), idx, t, rows, 2.0, 1.0, torch.bfloat16)
+    again = run_distill(opt, want, idx, t, rows, 2.0, 1.0, grad, in_place)
+    for a, b in zip(got, again):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_distill_loss_only_equals_loss_with_gradient():
     opt = handle([(1, 4)], 3, 40, 4)
     g = gen(41)
