@@ -138,7 +138,7 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
  *   row_loss  device float[rows], may be NULL.
  *   dZ     rows x V of `type`, row stride ldd; may be Z itself (same pointer
  *          and row stride).
- * temperature > 0, V >= 1, 1 <= K <= SIGNMUON_DISTILL_MAX_K (E_UNSUPPORTED).
+ * temperature > 0, 1 <= V <= 2^30, 1 <= K <= SIGNMUON_DISTILL_MAX_K (E_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t V, const void* idx,
                      int id_type, const void* t, int t_type, int64_t ldt, int K,

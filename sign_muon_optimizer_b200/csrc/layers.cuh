@@ -28,6 +28,10 @@ struct GradPtrs {     // per-worker gradient vectors, passed by value
 };
 
 #ifdef __CUDACC__
+// The kernels' read-only pointers are not __restrict__: of such a pointer the
+// compiler may read what it likes as early as it likes, before griddep_wait too,
+// when the kernel before this one is still writing it.
+
 // the m with pre[m] <= i < pre[m+1] (pre ascending, pre[0] = 0, i < pre[M])
 __device__ __forceinline__ int worker_of(const int* pre, int M, int i) {
   int lo = 0, hi = M - 1;
@@ -42,16 +46,19 @@ __device__ __forceinline__ int worker_of(const int* pre, int M, int i) {
 template <typename T> struct Elem;
 template <> struct Elem<float> {
   static constexpr int V = 4;   // elements in 16 bytes
+  static constexpr bool kHalf = false;
   static __device__ __forceinline__ float up(float x) { return x; }
   static __device__ __forceinline__ float down(float x) { return x; }
 };
 template <> struct Elem<__nv_bfloat16> {
   static constexpr int V = 8;
+  static constexpr bool kHalf = false;
   static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
 };
 template <> struct Elem<__half> {
   static constexpr int V = 8;
+  static constexpr bool kHalf = true;
   static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
 };

@@ -327,7 +327,7 @@ int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t
     TRY(ready(h));
     TRY(check_type(h, type));
     TRY(check_type(h, t_type));
-    if (V < 1 || V > INT_MAX) return fail(h, SIGNMUON_E_INVALID, "V must be in [1, 2^31)");
+    if (V < 1 || V > kMaxSize) return fail(h, SIGNMUON_E_INVALID, "V must be in [1, 2^30]");
     if (K < 1) return fail(h, SIGNMUON_E_INVALID, "K must be >= 1");
     if (K > SIGNMUON_DISTILL_MAX_K)
       return fail(h, SIGNMUON_E_UNSUPPORTED, "at most " + std::to_string(SIGNMUON_DISTILL_MAX_K) + " teacher entries a row");

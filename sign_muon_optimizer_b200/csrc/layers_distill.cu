@@ -151,57 +151,62 @@ struct Running {
 template <typename T>
 struct RowView {
   const T* z;
-  int mis, head, nv, tail, n_tail;   // tail = head + nv * V; n_tail elements from there on
-  __device__ __forceinline__ RowView(const T* row, int64_t V) : z(row) {
+  int mis, head, nv;
+  __device__ __forceinline__ RowView(const T* row, int V) : z(row) {
     constexpr int VL = Elem<T>::V;
     mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    head = (int)(V < (VL - mis) % VL ? V : (VL - mis) % VL);
-    nv = (int)((V - head) / VL);
-    tail = head + nv * VL;
-    n_tail = (int)(V - tail);
+    head = min(V, (VL - mis) % VL);
+    nv = (V - head) / VL;
   }
+  __device__ __forceinline__ int tail() const { return head + nv * Elem<T>::V; }
   __device__ __forceinline__ const Pack<T>* packs() const { return reinterpret_cast<const Pack<T>*>(z + head); }
 };
 
-constexpr int kAhead = 4;   // packs loaded before the first is used
+template <typename T>
+__device__ __forceinline__ void add_pack(const Pack<T>& p, F2 neg_ref, F2 c2, F2& sum) {
+#pragma unroll
+  for (int j = 0; j < Elem<T>::V / 2; ++j) {
+    const float2 x = unpack2(fma2(up2(p, j), c2, neg_ref));
+    sum = add2(pack2(ex2(x.x), ex2(x.y)), sum);
+  }
+}
 
-// Pass 1: packs tid, tid + THREADS, ... of nv into the running softmax;
-// after(i, n) follows when n packs from pack i on (THREADS apart) are done.
-template <typename T, int THREADS, typename F>
-__device__ __forceinline__ void absorb(Running& run, const Pack<T>* packs, int nv, int tid, float c, F after) {
-  constexpr int VL = Elem<T>::V;
-  const F2 c2 = pack2(c, c);
-  auto take = [&](const Pack<T>& p, F2 neg, F2& sum) {
+// N packs into the running softmax
+template <typename T, int N>
+__device__ __forceinline__ void add_packs(Running& run, const Pack<T>* p, float c) {
+  float t = pack_max(p[0]);
 #pragma unroll
-    for (int j = 0; j < VL / 2; ++j) {
-      const float2 x = unpack2(fma2(up2(p, j), c2, neg));
-      sum = add2(pack2(ex2(x.x), ex2(x.y)), sum);
-    }
-  };
+  for (int a = 1; a < N; ++a) t = fmaxf(t, pack_max(p[a]));
+  const float r = run.raise(t, c);
+  F2 sum = 0ull;
+#pragma unroll
+  for (int a = 0; a < N; ++a) add_pack(p[a], pack2(-r, -r), pack2(c, c), sum);
+  run.s += sum2(sum);
+}
+
+// packs tid, tid + THREADS, ... of nv into the running softmax; the first `hold`
+// packs of the row (a multiple of THREADS * AHEAD) are left in `held` too, each
+// in a place that only its thread reads
+template <typename T, int THREADS, int AHEAD>
+__device__ __forceinline__ void absorb(Running& run, const Pack<T>* packs, int nv, int tid, float c, Pack<T>* held, int hold) {
   int i = tid;
-  for (; i + (kAhead - 1) * THREADS < nv; i += kAhead * THREADS) {
-    Pack<T> p[kAhead];
-    const Pack<T>* from = packs + i;
+  for (; i < hold && i + (AHEAD - 1) * THREADS < nv; i += AHEAD * THREADS) {
+    Pack<T> p[AHEAD];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) p[a] = from[a * THREADS];
-    float t = pack_max(p[0]);
+    for (int a = 0; a < AHEAD; ++a) p[a] = packs[i + a * THREADS];
 #pragma unroll
-    for (int a = 1; a < kAhead; ++a) t = fmaxf(t, pack_max(p[a]));
-    const float r = run.raise(t, c);
-    const F2 neg = pack2(-r, -r);
-    F2 sum = 0ull;
+    for (int a = 0; a < AHEAD; ++a) held[i + a * THREADS] = p[a];
+    add_packs<T, AHEAD>(run, p, c);
+  }
+  for (; i + (AHEAD - 1) * THREADS < nv; i += AHEAD * THREADS) {
+    Pack<T> p[AHEAD];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) take(p[a], neg, sum);
-    run.s += sum2(sum);
-    after(i, kAhead);
+    for (int a = 0; a < AHEAD; ++a) p[a] = packs[i + a * THREADS];
+    add_packs<T, AHEAD>(run, p, c);
   }
   for (; i < nv; i += THREADS) {
     const Pack<T> p = packs[i];
-    const float r = run.raise(pack_max(p), c);
-    F2 sum = 0ull;
-    take(p, pack2(-r, -r), sum);
-    run.s += sum2(sum);
-    after(i, 1);
+    add_packs<T, 1>(run, &p, c);
   }
 }
 
@@ -252,46 +257,55 @@ struct Softmax {
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_pack(const Pack<T>& o, T* to) {
   if (ALIGNED) {
-    *reinterpret_cast<Pack<T>*>(to) = o;
+    __stcs(reinterpret_cast<uint4*>(to), reinterpret_cast<const uint4&>(o));   // (not to push logits out of L2)
   } else {
 #pragma unroll
     for (int j = 0; j < Elem<T>::V; ++j) to[j] = o.v[j];
   }
 }
 
-// Pass 2: the gradient of packs tid, tid + THREADS, ... to out; after as above
-template <typename T, int THREADS, bool ALIGNED, typename F>
+// the gradient of packs tid, tid + THREADS, ... to out; held and hold as above
+template <typename T, int THREADS, int AHEAD, bool ALIGNED>
 __device__ __forceinline__ void emit_grad(const Softmax<T>& x, float ws, const Pack<T>* packs, int nv, int tid, T* out,
-                                          F after) {
+                                          const Pack<T>* held, int hold) {
   constexpr int VL = Elem<T>::V;
   int i = tid;
-  for (; i + (kAhead - 1) * THREADS < nv; i += kAhead * THREADS) {
-    Pack<T> p[kAhead];
+  for (; i < hold && i + (AHEAD - 1) * THREADS < nv; i += AHEAD * THREADS) {
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      Pack<T> o;
+      x.pack(held[i + a * THREADS], ws, o);
+      store_pack<T, ALIGNED>(o, out + (int64_t)(i + a * THREADS) * VL);
+    }
+  }
+  for (; i + (AHEAD - 1) * THREADS < nv; i += AHEAD * THREADS) {
+    Pack<T> p[AHEAD];
     const Pack<T>* from = packs + i;
     T* to = out + (int64_t)i * VL;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) p[a] = from[a * THREADS];
+    for (int a = 0; a < AHEAD; ++a) {             // (read for the last time)
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(from + a * THREADS));
+      p[a] = reinterpret_cast<const Pack<T>&>(u);
+    }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
+    for (int a = 0; a < AHEAD; ++a) {
       Pack<T> o;
       x.pack(p[a], ws, o);
       store_pack<T, ALIGNED>(o, to + a * THREADS * VL);
     }
-    after(i, kAhead);
   }
   for (; i < nv; i += THREADS) {
     Pack<T> o;
     x.pack(packs[i], ws, o);
     store_pack<T, ALIGNED>(o, out + (int64_t)i * VL);
-    after(i, 1);
   }
 }
 
 // A far row's sum, from its maximum: (z - all) c cannot overflow upwards
 template <typename T, int WARPS, typename F>
-__device__ __forceinline__ float far_sum(const T* z, int64_t V, int tid, float all, float c, float2* buf, F barrier) {
+__device__ __forceinline__ float far_sum(const T* z, int V, int tid, float all, float c, float2* buf, F barrier) {
   float s = 0.f;
-  for (int64_t v = tid; v < V; v += WARPS * 32) s += ex2((Elem<T>::up(z[v]) - all) * c);
+  for (int v = tid; v < V; v += WARPS * 32) s += ex2((Elem<T>::up(z[v]) - all) * c);
   s = warp_sum(s);
   if (WARPS > 1) {
     barrier();                      // buf has been read
@@ -305,9 +319,11 @@ __device__ __forceinline__ float far_sum(const T* z, int64_t V, int tid, float a
 // A row's entries in shared memory, K of each: index (-1: absent), probability
 // and the student's logit there.
 struct Entries {
-  int* id;
-  float *q, *zk;
-  __device__ __forceinline__ Entries(float* at, int K) : id(reinterpret_cast<int*>(at)), q(at + K), zk(at + 2 * K) {}
+  float* at;
+  int K;
+  __device__ __forceinline__ int& id(int k) const { return reinterpret_cast<int*>(at)[k]; }
+  __device__ __forceinline__ float& q(int k) const { return at[K + k]; }
+  __device__ __forceinline__ float& zk(int k) const { return at[2 * K + k]; }
 };
 
 // an entry as it is read: its index, or -1, and its logit
@@ -315,122 +331,155 @@ struct Entry {
   int id;
   float t;
 };
-__device__ __forceinline__ Entry load_entry(const Teacher& te, int r, int k, int64_t V) {
+__device__ __forceinline__ Entry load_entry(const Teacher& te, int r, int k, int V) {
   const int64_t i = load_id(te.idx, te.id64, (int64_t)r * te.ldt + k);
   const float t = load_t(te.t, te.t_type, (int64_t)r * te.ldt + k);
   return Entry{counts(i, V, t) ? (int)i : -1, t};
 }
 
-// Entry k into shared memory; returns its part q log q of the loss.
-__device__ __forceinline__ float put_entry(const Entries& e, int k, const Entry& x, float zk, const RowStat& st, float inv_T) {
-  const float lq = (x.t - st.top) * inv_T - st.log_sum;
-  const float q = x.id >= 0 ? expf(lq) : 0.f;
-  e.id[k] = x.id;
-  e.q[k] = q;
-  e.zk[k] = zk;
+// Entry k's logit in e.q becomes its probability; returns its part q log q of the loss.
+__device__ __forceinline__ float weigh_entry(const Entries& e, int k, const RowStat& st, float inv_T) {
+  const float lq = (e.q(k) - st.top) * inv_T - st.log_sum;
+  const float q = e.id(k) >= 0 ? expf(lq) : 0.f;
+  e.q(k) = q;
   return q == 0.f ? 0.f : q * lq;
 }
 
 // entry k's part -q log p of the loss (q = 0: nothing, whatever p is)
 template <typename T>
 __device__ __forceinline__ float cross(const Entries& e, int k, const Softmax<T>& x, float log2_s) {
-  const float q = e.q[k];
-  return q == 0.f ? 0.f : q * ((log2_s - x.log2_e(e.zk[k])) * 0.6931471805599453f);
+  const float q = e.q(k);
+  return q == 0.f ? 0.f : q * ((log2_s - x.log2_e(e.zk(k))) * 0.6931471805599453f);
 }
 
 // The gradient at entry k, w (p - q).  Where an index may be there twice, the
 // first of its entries writes for all.
 template <typename T>
 __device__ __forceinline__ void correct(const Entries& e, int K, int k, bool twice, const Softmax<T>& x, float w, T* dz) {
-  const int id = e.id[k];
+  const int id = e.id(k);
   if (id < 0) return;
   bool mine = true;
-  float sum = e.q[k];
+  float sum = e.q(k);
   if (twice) {
     sum = 0.f;
     for (int i = 0; i < K; ++i)
-      if (e.id[i] == id) {
+      if (e.id(i) == id) {
         if (i < k) mine = false;
-        sum += e.q[i];
+        sum += e.q(i);
       }
   }
-  if (mine) dz[id] = Elem<T>::down(w * (ex2(x.log2_e(e.zk[k])) / x.s - sum));
+  if (mine) dz[id] = Elem<T>::down(w * (ex2(x.log2_e(e.zk(k))) / x.s - sum));
 }
 
 template <typename T>
-__device__ __forceinline__ void zero_row(T* dz, int64_t V, int tid, int threads) {
+__device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
   const RowView<T> v(dz, V);
   Pack<T> o;
 #pragma unroll
   for (int j = 0; j < Elem<T>::V; ++j) o.v[j] = Elem<T>::down(0.f);
   for (int i = tid; i < v.nv; i += threads) *reinterpret_cast<Pack<T>*>(dz + v.head + (int64_t)i * Elem<T>::V) = o;
   if (tid < v.head) dz[tid] = o.v[0];
-  if (tid < v.n_tail) dz[v.tail + tid] = o.v[0];
+  if (v.tail() + tid < V) dz[v.tail() + tid] = o.v[0];
 }
 
-// ROW_THREADS threads hold a row: a block (rows too long for shared memory), or
-// a warp (short rows, four a block).  The row is read twice, for the maximum
-// and sum of the softmax and for the gradient (the second time from L2).
+// ROW_THREADS threads take a row: a block, or a warp (short rows, four a block).
+// Bound by the bytes: the row is read for the maximum and sum of the softmax,
+// and a second time, from L2, for the gradient, which is written.  What counts
+// is that there are always loads on their way: several blocks on an SM, in
+// different parts of their rows, do better than rows kept in shared memory and
+// loaded a row ahead, of which two fit (8192 x 32003 bf16, 64 entries: 217 us
+// against 262), because those fall into step, all waiting for memory and then
+// all computing.
+// The first blocks start before k_distill_teacher is done (everything before it
+// is) and wait for it where they need its results; behind them rows without
+// entries are known before their logits are read.
+constexpr int kBlocks = 5;      // of 256 threads on an SM
+// the registers that this leaves are enough (fp16's conversions take more)
 template <typename T, int ROW_THREADS>
-__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THREADS == 32 ? 6 : 3)
-    k_distill_rows(const RowMap map, const Teacher te, const RowStat* __restrict__ stat, const int* __restrict__ kinds,
-                   const T* Z, int64_t ldz, int64_t V, float temperature, float gscale, const int* __restrict__ count,
-                   float* __restrict__ row_loss, T* dZ, int64_t ldd) {
+constexpr int min_blocks() {
+  return ROW_THREADS == 32 ? 9 : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
+}
+constexpr int kAhead = 2;       // packs a thread loads before it uses the first
+template <typename T, int ROW_THREADS, bool GRAD>
+__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blocks<T, ROW_THREADS>())
+    k_distill_rows(const RowMap map, const Teacher te, const RowStat* stat, const int* kinds,
+                   const T* Z, int64_t ldz, int V, float temperature, float gscale, const int* count,
+                   float* __restrict__ row_loss, T* dZ, int64_t ldd, int early, int hold) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
-  extern __shared__ float entries[];              // per row: 3 arrays of K
+  extern __shared__ uint4 shared[];               // `hold` packs; per row: 3 arrays of K
   __shared__ float2 buf[WARPS];
   __shared__ float losses[WARPS];
-  griddep_wait();
+  const bool first = (int)blockIdx.x < early;
+  if (!first) griddep_wait();
   griddep_launch();
   const int tid = threadIdx.x % ROW_THREADS, in_block = threadIdx.x / ROW_THREADS;
   const int r = blockIdx.x * ROWS + in_block;
-  if (r >= map.start[map.M]) return;              // (a whole warp)
-  const Entries e(entries + (int64_t)in_block * 3 * te.K, te.K);
+  const int K = te.K;
+  Pack<T>* held = reinterpret_cast<Pack<T>*>(shared);
+  float* entries = reinterpret_cast<float*>(shared + hold);
   auto sync = [&] {
     if (ROW_THREADS == 32) __syncwarp();
     else __syncthreads();
   };
   const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
+  if (r >= map.start[map.M]) {                    // (a whole warp)
+    if (first) griddep_wait();
+    return;
+  }
+  T* dz = GRAD ? dZ + (int64_t)r * ldd : nullptr;
+  int kind = first ? (int)ROW_ONCE : kinds[r];
   const RowView<T> v(Z + (int64_t)r * ldz, V);
-  T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
-  const int kind = kinds[r];
+  const Entries e{entries + in_block * 3 * K, K};
+  if (kind != ROW_NONE) {
+    for (int k = tid; k < K; k += ROW_THREADS) {
+      const Entry x = load_entry(te, r, k, V);
+      e.id(k) = x.id;
+      e.q(k) = x.t;
+      e.zk(k) = x.id >= 0 ? Elem<T>::up(v.z[x.id]) : 0.f;
+    }
+  }
+  Running run;
+  if (kind != ROW_NONE) {
+    absorb<T, ROW_THREADS, kAhead>(run, v.packs(), v.nv, tid, c, held, GRAD ? hold : 0);
+    if (tid < v.head) run.one(Elem<T>::up(v.z[tid]), c);
+    if (v.tail() + tid < V) run.one(Elem<T>::up(v.z[v.tail() + tid]), c);
+  }
+  if (first) {
+    griddep_wait();
+    kind = kinds[r];
+  }
   if (kind == ROW_NONE) {
-    if (dz != nullptr) zero_row(dz, V, tid, ROW_THREADS);
+    if (GRAD) zero_row(dz, V, tid, ROW_THREADS);
     if (tid == 0) row_loss[r] = 0.f;
     return;
   }
   float loss = 0.f;
-  {
+  if (tid < K) {
     const RowStat st = stat[r];
-    for (int k = tid; k < te.K; k += ROW_THREADS) {
-      const Entry x = load_entry(te, r, k, V);
-      loss += put_entry(e, k, x, x.id >= 0 ? Elem<T>::up(v.z[x.id]) : 0.f, st, inv_T);
-    }
+    for (int k = tid; k < K; k += ROW_THREADS) loss += weigh_entry(e, k, st, inv_T);
   }
-  Running run;
-  absorb<T, ROW_THREADS>(run, v.packs(), v.nv, tid, c, [](int, int) {});
-  if (tid < v.head) run.one(Elem<T>::up(v.z[tid]), c);
-  if (tid < v.n_tail) run.one(Elem<T>::up(v.z[v.tail + tid]), c);
   float all, s;
   join_row<WARPS>(run, tid, c, buf, sync, all, s);
   Softmax<T> x(all, s, c);
   if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf, sync);
-  const float log2_s = log2f(x.s);
-  for (int k = tid; k < te.K; k += ROW_THREADS) loss += cross(e, k, x, log2_s);
-  loss = warp_sum(loss);
+  if ((tid & ~31) < K) {                          // (warps beyond K have nothing to add)
+    const float log2_s = log2f(x.s);
+    for (int k = tid; k < K; k += ROW_THREADS) loss += cross(e, k, x, log2_s);
+    loss = warp_sum(loss);
+  }
   if (WARPS > 1 && (tid & 31) == 0) losses[tid >> 5] = loss;
-  if (dz != nullptr) {
+  if (GRAD) {
     const float w = gscale * temperature / (float)count[worker_of(map.start, map.M, r)], ws = w / x.s;
     if (x.far) {
-      for (int64_t i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
+      for (int i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
     } else {
-      if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, ROW_THREADS, true>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
-      else emit_grad<T, ROW_THREADS, false>(x, ws, v.packs(), v.nv, tid, dz + v.head, [](int, int) {});
+      if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, ROW_THREADS, kAhead, true>(x, ws, v.packs(), v.nv, tid, dz + v.head, held, hold);
+      else emit_grad<T, ROW_THREADS, kAhead, false>(x, ws, v.packs(), v.nv, tid, dz + v.head, held, hold);
       if (tid < v.head) dz[tid] = x.grad(Elem<T>::up(v.z[tid]), w);
-      if (tid < v.n_tail) dz[v.tail + tid] = x.grad(Elem<T>::up(v.z[v.tail + tid]), w);
+      if (v.tail() + tid < V) dz[v.tail() + tid] = x.grad(Elem<T>::up(v.z[v.tail() + tid]), w);
     }
     sync();
-    for (int k = tid; k < te.K; k += ROW_THREADS) correct(e, te.K, k, kind == ROW_TWICE, x, w, dz);
+    for (int k = tid; k < K; k += ROW_THREADS) correct(e, K, k, kind == ROW_TWICE, x, w, dz);
   } else {
     sync();
   }
@@ -443,133 +492,8 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, ROW_THR
   }
 }
 
-// A block stays and takes row after row, each in shared memory: the next row
-// comes in through asynchronous copies while this one's gradient goes out (or,
-// for the loss alone, while its sum is made), pack by pack into the places that
-// the same thread has just read.  The next row's entries are loaded a row ahead
-// too, the logits there at the row's start.  Two blocks on an SM.
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 128 ? 2 : 6)
-    k_distill_resident(const RowMap map, const Teacher te, const RowStat* __restrict__ stat,
-                       const int* __restrict__ kinds, const T* Z, int64_t ldz, int64_t V, int slots, float temperature,
-                       float gscale, const int* __restrict__ count, float* __restrict__ row_loss, T* dZ, int64_t ldd) {
-  constexpr int WARPS = THREADS / 32;
-  extern __shared__ uint4 row_at[];               // `slots` packs, then twice 3 arrays of K
-  __shared__ float2 buf[2][WARPS];
-  __shared__ float losses[2][WARPS];
-  griddep_wait();
-  griddep_launch();
-  float* entries = reinterpret_cast<float*>(row_at + slots);
-  const int N = map.start[map.M], step = gridDim.x;
-  const int tid = threadIdx.x, K = te.K;
-  const float inv_T = 1.f / temperature, c = inv_T * 1.4426950408889634f;
-  const Pack<T>* packs = reinterpret_cast<const Pack<T>*>(row_at);
-  auto sync = [] { __syncthreads(); };
-  const unsigned slot = (unsigned)__cvta_generic_to_shared(row_at);
-  // packs i, i + THREADS, ..., n of them, of the next row
-  auto fetch = [&](const Pack<T>* from, int nv, int i, int n) {
-    from += i;
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (a < n && i + a * THREADS < nv)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (i + a * THREADS) * 16), "l"(from + a * THREADS)
-                     : "memory");
-  };
-  auto finish_loss = [&](int r, int b) {          // thread 0, behind a barrier
-    float t = 0.f;
-    for (int i = 0; i < WARPS; ++i) t += losses[b][i];
-    row_loss[r] = t * (temperature * temperature);
-  };
-  int b = 0, r = blockIdx.x;
-  // this row's and the next one's kind; this row's first entry of the thread
-  int kind = kinds[r], kind1 = r + step < N ? kinds[r + step] : ROW_NONE;
-  Entry x0 = tid < K ? load_entry(te, r, tid, V) : Entry{-1, 0.f};
-  RowStat st = stat[r];
-  if (kind != ROW_NONE) {
-    const RowView<T> v(Z + (int64_t)r * ldz, V);
-    for (int i = tid; i < v.nv; i += THREADS) fetch(v.packs(), v.nv, i, 1);
-  }
-  for (; r < N; r += step) {
-    const RowView<T> v(Z + (int64_t)r * ldz, V);
-    const Entries e(entries + b * 3 * K, K);
-    // loads whose results are wanted later: the logits at the entries, the
-    // row's edges, the worker's count; the next row's first entries, the kind
-    // of the row behind it
-    const float zk = kind != ROW_NONE && x0.id >= 0 ? Elem<T>::up(v.z[x0.id]) : 0.f;
-    const float edge0 = tid < v.head ? Elem<T>::up(v.z[tid]) : -INFINITY;
-    const float edge1 = tid < v.n_tail ? Elem<T>::up(v.z[v.tail + tid]) : -INFINITY;
-    const float n = dZ != nullptr ? (float)count[worker_of(map.start, map.M, r)] : 1.f;
-    const int64_t r1 = (int64_t)r + step, r2 = r1 + step;
-    Entry x1{-1, 0.f};
-    RowStat st1 = st;
-    if (r1 < N) {
-      if (tid < K) x1 = load_entry(te, (int)r1, tid, V);
-      st1 = stat[r1];
-    }
-    const int kind2 = r2 < N ? kinds[r2] : ROW_NONE;
-    const RowView<T> next(Z + (r1 < N ? r1 : (int64_t)r) * ldz, V);
-    const Pack<T>* next_packs = next.packs();
-    const int next_nv = kind1 != ROW_NONE ? next.nv : 0;
-    auto after = [&](int i, int k) { fetch(next_packs, next_nv, i, k); };
-    T* dz = dZ != nullptr ? dZ + (int64_t)r * ldd : nullptr;
-    if (kind != ROW_NONE) {
-      copy_commit();
-      copy_wait<0>();
-      Running run;
-      if (dz != nullptr) absorb<T, THREADS>(run, packs, v.nv, tid, c, [](int, int) {});
-      else absorb<T, THREADS>(run, packs, v.nv, tid, c, after);
-      if (tid < v.head) run.one(edge0, c);
-      if (tid < v.n_tail) run.one(edge1, c);
-      float loss = 0.f;
-      if (tid < K) loss = put_entry(e, tid, x0, zk, st, inv_T);
-      for (int k = tid + THREADS; k < K; k += THREADS) {
-        const Entry y = load_entry(te, r, k, V);
-        loss += put_entry(e, k, y, y.id >= 0 ? Elem<T>::up(v.z[y.id]) : 0.f, st, inv_T);
-      }
-      float all, s;
-      join_row<WARPS>(run, tid, c, buf[b], sync, all, s);
-      Softmax<T> x(all, s, c);
-      if (x.far) x.s = far_sum<T, WARPS>(v.z, V, tid, all, c, buf[b], sync);
-      const float log2_s = log2f(x.s);
-      for (int k = tid; k < K; k += THREADS) loss += cross(e, k, x, log2_s);
-      loss = warp_sum(loss);
-      if ((tid & 31) == 0) losses[b][tid >> 5] = loss;
-      int done = tid;                             // the first pack of this thread's that is not yet sent for
-      while (done < v.nv) done += THREADS;
-      if (dz != nullptr) {
-        const float w = gscale * temperature / n, ws = w / x.s;
-        if (x.far) {
-          for (int64_t i = tid; i < V; i += THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
-          done = tid;
-        } else {
-          if (RowView<T>(dz, V).mis == v.mis) emit_grad<T, THREADS, true>(x, ws, packs, v.nv, tid, dz + v.head, after);
-          else emit_grad<T, THREADS, false>(x, ws, packs, v.nv, tid, dz + v.head, after);
-          if (tid < v.head) dz[tid] = x.grad(edge0, w);
-          if (tid < v.n_tail) dz[v.tail + tid] = x.grad(edge1, w);
-        }
-        for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
-        __syncthreads();                          // the row's gradient is written
-        for (int k = tid; k < K; k += THREADS) correct(e, K, k, kind == ROW_TWICE, x, w, dz);
-      } else {
-        for (; done < next_nv; done += THREADS) fetch(next_packs, next_nv, done, 1);
-        __syncthreads();                          // the row's losses are in place
-      }
-      if (tid == 0) finish_loss(r, b);
-      b ^= 1;                                     // two barriers lie before these buffers are used again
-    } else {
-      if (dz != nullptr) zero_row(dz, V, tid, THREADS);
-      if (tid == 0) row_loss[r] = 0.f;
-      for (int i = tid; i < next_nv; i += THREADS) fetch(next_packs, next_nv, i, 1);
-    }
-    kind = kind1;
-    kind1 = kind2;
-    x0 = x1;
-    st = st1;
-  }
-}
-
 // loss[m], count[m]; leaves the counters at zero for the next call
-__global__ void __launch_bounds__(256) k_distill_loss(const RowMap map, const float* __restrict__ row_loss, int* count,
+__global__ void __launch_bounds__(256) k_distill_loss(const RowMap map, const float* row_loss, int* count,
                                                       float* __restrict__ loss, int32_t* __restrict__ count_out) {
   __shared__ double buf[256];
   griddep_wait();
@@ -596,47 +520,48 @@ struct Scratch {
   int* kind;
 };
 
-template <typename T, int ROW_THREADS>
+constexpr int64_t kL2Bytes = 50'000'000;
+
+template <typename T, int ROW_THREADS, bool GRAD>
 void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1;
-  const size_t smem = (size_t)ROWS * 3 * a.K * 4;
-  auto* kernel = k_distill_rows<T, ROW_THREADS>;
+  size_t smem = (size_t)ROWS * 3 * a.K * 4;
+  auto* kernel = k_distill_rows<T, ROW_THREADS, GRAD>;
+  int hold = 0;
+  if (GRAD && ROW_THREADS == 256) {
+    // What the rows on their way have in L2 must stay within half of it, or the
+    // second reading misses it: where kBlocks rows an SM are too much, their
+    // first packs are held in shared memory (8192 x 50304 bf16: 369 -> 351 us),
+    // and the longest rows go with fewer blocks.
+    const int64_t row = a.V * (int64_t)sizeof(T);
+    for (int blocks = kBlocks; blocks >= 1; --blocks) {
+      const int64_t room = (int64_t)226 * 1024 / blocks - 1536 - (int64_t)smem;
+      const int64_t fits = row / 16 / (ROW_THREADS * kAhead) * (ROW_THREADS * kAhead), can = room / 16 / (ROW_THREADS * kAhead) * (ROW_THREADS * kAhead);
+      if (blocks == kBlocks && num_sms() * blocks * row <= kL2Bytes) break;
+      hold = (int)(can < 0 ? 0 : can < fits ? can : fits);
+      if (blocks == 1 || num_sms() * blocks * (row - hold * (int64_t)16) <= kL2Bytes) break;
+    }
+    smem += (size_t)hold * 16;
+  }
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int blocks = (map.start[map.M] + ROWS - 1) / ROWS;
+  const int early = num_sms() * resident_per_sm((const void*)kernel, ROWS * ROW_THREADS, smem);
   count_launch();
-  launch_pdl(kernel, dim3((map.start[map.M] + ROWS - 1) / ROWS), dim3(ROWS * ROW_THREADS), smem, s, map, te,
-             (const RowStat*)x.stat, (const int*)x.kind, reinterpret_cast<const T*>(a.Z), a.ldz, a.V, a.temperature,
-             a.gscale, (const int*)a.count, a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd);
+  launch_pdl(kernel, dim3(blocks), dim3(ROWS * ROW_THREADS), smem, s, map, te, (const RowStat*)x.stat,
+             (const int*)x.kind, reinterpret_cast<const T*>(a.Z), a.ldz, (int)a.V, a.temperature, a.gscale,
+             (const int*)a.count, a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd, early,
+             hold);
 }
 
-int resident_slots(const DistillArgs& a, int elem, int threads) {
-  const int64_t packs = a.V * elem / 16;
-  return (int)((packs + threads - 1) / threads * threads);
-}
-
-template <typename T, int THREADS>
-void run_resident(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
-  auto* kernel = k_distill_resident<T, THREADS>;
-  const int slots = resident_slots(a, sizeof(T), THREADS);
-  const size_t smem = (size_t)slots * 16 + (size_t)2 * 3 * a.K * 4;
-  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  const int grid = stream_grid((const void*)kernel, THREADS, smem, map.start[map.M], 16);
-  count_launch();
-  launch_pdl(kernel, dim3(grid), dim3(THREADS), smem, s, map, te, (const RowStat*)x.stat, (const int*)x.kind,
-             reinterpret_cast<const T*>(a.Z), a.ldz, a.V, slots, a.temperature, a.gscale, (const int*)a.count,
-             a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd);
-}
-
-// A warp for the shortest rows, so that most of it has something to load; rows
-// of which two fit an SM's shared memory stay there; longer ones are read twice.
-constexpr int64_t kResidentBytes = 112 * 1024;
-constexpr int kLong = 256;
-template <typename T>
+// Few threads for short rows, so that each has something to load: 16384 rows
+// with gradient of 4000 bf16 take 71 / 91 / 135 us with 32 / 128 / 256 threads,
+// of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382.
+template <typename T, bool GRAD>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
-  const int64_t fixed = (int64_t)2 * 3 * a.K * 4 + 512;
-  if (a.V <= 1024) run_rows<T, 32>(s, a, map, te, x);
-  else if (a.V <= 8192) run_resident<T, 128>(s, a, map, te, x);
-  else if (a.V * (int64_t)sizeof(T) + 16 * kLong + fixed <= kResidentBytes) run_resident<T, kLong>(s, a, map, te, x);
-  else run_rows<T, kLong>(s, a, map, te, x);
+  const int64_t row = a.V * (int64_t)sizeof(T);
+  if (row <= 16 * 1024) run_rows<T, 32, GRAD>(s, a, map, te, x);
+  else if (row <= 48 * 1024) run_rows<T, 128, GRAD>(s, a, map, te, x);
+  else run_rows<T, 256, GRAD>(s, a, map, te, x);
 }
 
 }  // namespace
@@ -657,9 +582,11 @@ void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int 
     else
       launch_pdl(k_distill_teacher<256>, dim3(N), dim3(256), 0, s, map, te, a.V, inv_T, x.stat, x.kind, a.count,
                  a.status);
-    if (a.type == LT_F32) pick_rows<float>(s, a, map, te, x);
-    else if (a.type == LT_BF16) pick_rows<__nv_bfloat16>(s, a, map, te, x);
-    else pick_rows<__half>(s, a, map, te, x);
+#define SM_PICK(T) (a.dZ != nullptr ? pick_rows<T, true>(s, a, map, te, x) : pick_rows<T, false>(s, a, map, te, x))
+    if (a.type == LT_F32) SM_PICK(float);
+    else if (a.type == LT_BF16) SM_PICK(__nv_bfloat16);
+    else SM_PICK(__half);
+#undef SM_PICK
   }
   count_launch();
   launch_pdl(k_distill_loss, dim3(M), dim3(256), 0, s, map, (const float*)a.row_loss, a.count, a.loss, a.count_out);

@@ -15,8 +15,8 @@ namespace {
 constexpr int kSlab = 1024;
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_embed(const float* __restrict__ table, int64_t V, int E,
-                                               const void* __restrict__ ids, int id64, int64_t n, int n_slab,
+__global__ void __launch_bounds__(256) k_embed(const float* table, int64_t V, int E,
+                                               const void* ids, int id64, int64_t n, int n_slab,
                                                float scale, T* __restrict__ out, int64_t ld, int* status) {
   griddep_wait();
   griddep_launch();
@@ -80,7 +80,7 @@ __device__ __forceinline__ K shfl_xor(K v, int lanes) {
 constexpr int kPlaceBits = 11;
 static_assert(kSortTile == 1 << kPlaceBits, "a place in the tile has kPlaceBits bits");
 template <typename K>
-__global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, const void* __restrict__ ids, int id64,
+__global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, const void* ids, int id64,
                                                              int64_t V, Key* __restrict__ keys, int* status) {
   constexpr int THREADS = kSortThreads;
   constexpr int PER = kSortTile / THREADS;
@@ -172,7 +172,7 @@ __device__ __forceinline__ unsigned radix_id(const void* ids, int id64, int64_t 
   return (unsigned)(id >= 0 && id < V ? id : V);
 }
 
-__global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const void* __restrict__ ids, int id64, int64_t V,
+__global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const void* ids, int id64, int64_t V,
                                                      int bits, int digits, int* __restrict__ count, int64_t set,
                                                      int* status) {
   __shared__ int c[kBins];
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const voi
 }
 
 // src = null: the first digit, keys from the ids; next = null: the last digit
-__global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const void* __restrict__ ids, int id64,
-                                                       int64_t V, int shift, int bits, const Key* __restrict__ src,
+__global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const void* ids, int id64,
+                                                       int64_t V, int shift, int bits, const Key* src,
                                                        Key* __restrict__ dst, int* __restrict__ count,
                                                        int* __restrict__ next) {
   constexpr int ROUNDS = kRadixTile / 256;
@@ -292,7 +292,7 @@ struct ZeroRows {
   int64_t off, V;
 };
 
-__device__ __forceinline__ void zero_rows(const RowMap& map, const GradPtrs& G, const Key* __restrict__ keys, int E,
+__device__ __forceinline__ void zero_rows(const RowMap& map, const GradPtrs& G, const Key* keys, int E,
                                           const ZeroRows& z, int b, unsigned char* empty) {
   const int m = b / z.groups;
   const int64_t v0 = (int64_t)(b - m * z.groups) * z.rows;
@@ -348,8 +348,8 @@ __device__ __forceinline__ void emit(float* row, int c, int E, int lane, const f
 // a block per (unit of 8 * per_warp sorted tokens, strip of columns); the
 // blocks behind them zero the rows without tokens
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
-                                                      const T* __restrict__ dY, int64_t ld, int E, int n_strip,
+__global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* keys,
+                                                      const T* dY, int64_t ld, int E, int n_strip,
                                                       int64_t off, float scale, int accumulate,
                                                       float* __restrict__ part, int per_warp, int every,
                                                       const ZeroRows zero) {
@@ -472,9 +472,9 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
 // a warp per (unit, strip): where a run starts in the unit and goes on behind
 // it, its parts are added up in order and written
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const GradPtrs G, const Key* __restrict__ keys,
+__global__ void __launch_bounds__(256) k_embed_join(const RowMap map, const GradPtrs G, const Key* keys,
                                                     int E, int n_strip, int64_t off, float scale, int accumulate,
-                                                    const float* __restrict__ part, int unit) {
+                                                    const float* part, int unit) {
   constexpr int VL = Elem<T>::V;
   griddep_wait();
   griddep_launch();

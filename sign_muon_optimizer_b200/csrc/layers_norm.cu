@@ -16,8 +16,8 @@ constexpr int kStages = 3;
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC, int WPR, int EPL>
 __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
-    k_ln_fwd(const T* __restrict__ X, int64_t ldx, T* __restrict__ Y, int64_t ldy, const float* __restrict__ gamma,
-             const float* __restrict__ beta, int64_t n, int E, float eps, float* __restrict__ mean,
+    k_ln_fwd(const T* X, int64_t ldx, T* __restrict__ Y, int64_t ldy, const float* gamma,
+             const float* beta, int64_t n, int E, float eps, float* __restrict__ mean,
              float* __restrict__ rstd) {
   constexpr int VL = Elem<T>::V;
   constexpr int CH = EPL / VL;                      // strips per warp

@@ -23,8 +23,8 @@ constexpr int kStages = 3;
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC, int WPR, int EPL>
 __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
-    k_ln_bwd(const RowMap map, int rows_per_unit, const T* __restrict__ X, int64_t ldx, const T* dY, int64_t ldy,
-             const float* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
+    k_ln_bwd(const RowMap map, int rows_per_unit, const T* X, int64_t ldx, const T* dY, int64_t ldy,
+             const float* gamma, const float* mean, const float* rstd, T* dX,
              int64_t ldd, int E, float* __restrict__ part) {
   constexpr int VL = Elem<T>::V;
   constexpr int CH = EPL / VL;                      // strips per warp
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
 
 // G[m] (+)= the sum of worker m's blocks, in order: 32 columns a block, 8
 // threads a column, each over a fixed share of the blocks
-__global__ void __launch_bounds__(256) k_ln_weights(const RowMap map, const GradPtrs G, const float* __restrict__ part,
+__global__ void __launch_bounds__(256) k_ln_weights(const RowMap map, const GradPtrs G, const float* part,
                                                     int E, int64_t off_gamma, int64_t off_beta, int accumulate) {
   __shared__ float t[8][33];
   griddep_wait();
