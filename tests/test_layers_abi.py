@@ -144,3 +144,19 @@ def test_rows_default_to_equal_shares():
     with pytest.raises(ValueError):
         layers._share(opt(), None, 7)
     assert list(layers._share(opt(), None, 8)) == [4, 4]
+
+
+def test_no_layer_kernel_spills_or_keeps_a_stack_frame(tmp_path):
+    from concurrent.futures import ThreadPoolExecutor
+
+    import test_build_resources as resources
+    nvcc = resources._nvcc()
+    if nvcc is None:
+        pytest.skip("no nvcc")
+    sources = sorted(f for f in os.listdir(resources.CSRC) if f.startswith("layers_") and f != "layers_api.cu" and f.endswith(".cu"))
+    assert len(sources) == 4
+    with ThreadPoolExecutor(max_workers=4) as ex:
+        reports = list(ex.map(lambda s: resources._ptxas_report(nvcc, s, str(tmp_path)), sources))
+    found = {name: frame for rep in reports for name, (frame, _) in rep.items()}
+    assert len(found) >= 60
+    assert not {name: frame for name, frame in found.items() if frame != (0, 0, 0)}
