@@ -662,6 +662,61 @@ def run_ours(args):
     return 0
 
 
+def measure_layers(smo, stream, pk):
+    """The calls of a training pass that are not weight products, M = 8 workers
+    x 1024 tokens on a 50304 x 768 table and one layer norm (bf16
+    activations): each call alone, then the chain lookup -> layer norm ->
+    distillation loss with gradient (given logits) -> layer norm and table
+    gradients per worker -> signSGD step (K = 0, ternary signs) on them."""
+    import torch
+    V, E, M, N, K = 50304, 768, 8, 8192, 64
+    shapes = [(V, E), (1, E), (1, E)]
+    h = smo.SignMuon(shapes, M, beta=HP["beta"], lam=0.0, K=0, eps=HP["eps"], scale="fro",
+                     flags=smo.SIGNMUON_TERNARY | smo.SIGNMUON_ASYNC, stream=stream.cuda_stream)
+    h.layers_reserve(N, E)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    dev = dict(device="cuda", generator=g)
+    W = synth.device_weights0(shapes, config_id=8)
+    W[V * E:V * E + E] += 1
+    G = [torch.zeros(h.d, device="cuda") for _ in range(M)]
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    ids = ((V + 1.0) ** torch.rand(N, dtype=torch.float64, **dev)).long().clamp_(1, V) - 1
+    X, Y, dY, dX = (torch.empty(N, E, **bf) for _ in range(4))
+    dY.normal_(generator=g)
+    Z, dZ = torch.randn(N, V, dtype=torch.bfloat16, **dev), torch.empty(N, V, **bf)
+    idx = torch.randint(0, V, (N, K), **dev).int()
+    t = torch.randn(N, K, **dev)
+    mean, rstd, loss = (torch.empty(n, device="cuda") for n in (N, N, M))
+    calls = {
+        "embed": (lambda: h.embed(W, 0, ids, X, scale=E ** 0.5), N * E * 2 + min(N, V) * E * 4 + 8 * N),
+        "layernorm": (lambda: h.layernorm(W, 1, 2, X, Y, mean, rstd), 2 * N * E * 2 + 8 * N + 8 * E),
+        "distill": (lambda: h.distill(Z, idx, t, loss, dZ=dZ, temperature=2.0), 2 * N * V * 2 + 8 * N * K),
+        "layernorm_grad": (lambda: h.layernorm_grad(W, 1, 2, X, dY, mean, rstd, dX, G), 3 * N * E * 2 + 8 * N + 8 * M * E),
+        "embed_grad": (lambda: h.embed_grad(0, ids, dX, G, scale=E ** 0.5), N * E * 2 + 8 * N + 4 * M * V * E),
+        "step": (lambda: h.step(W, G, HP["eta"]), None),
+    }
+
+    def chain():
+        for f, _ in calls.values():
+            f()
+    out = []
+    for name, (f, nbytes) in calls.items():
+        ms = _events_time(f, 10, stream)
+        e = {"metric": f"layer call {name} (M=8 x 1024 tokens, 50304 x 768, bf16), us", "value": ms * 1e3, "unit": "us"}
+        if nbytes:
+            e.update({"GB/s": nbytes / ms / 1e6, "frac_of_hbm": nbytes / ms / 1e6 / pk["hbm_gbs"]})
+        out.append(e)
+    ms = _events_time(chain, 10, stream)
+    out.append({"metric": "pass over the layer calls and signSGD step (M=8 x 1024 tokens, 50304 x 768, bf16), ms",
+                "value": ms, "unit": "ms"})
+    h.sync()
+    h.layers_sync()
+    h.close()
+    torch.cuda.empty_cache()
+    return out
+
+
 def run_secondary(args):
     """Secondary measurements (not the headline line): the LLaMA-layer vote
     (vote GB/s, one-bit and int8 ternary signs), the Newton-Schulz sweep (NS
@@ -761,6 +816,8 @@ def run_secondary(args):
         torch.cuda.empty_cache()
     if args.workload in ("resnet50", "all"):
         lines.append(measure_resnet50(smo, stream, pk))
+    if args.workload in ("layers", "all"):
+        lines.extend(measure_layers(smo, stream, pk))
     if args.workload in ("cublas", "all"):
         c = measure_cublas_same_shapes(stream, pk)
         lines.append(dict({"metric": "cuBLAS TFLOP/s on the nanoGPT step's Newton-Schulz shapes (M=8, bf16)",
@@ -861,7 +918,7 @@ def main():
     ap.add_argument("--capture-variant", default="nanogpt", choices=["nanogpt", "ternary", "ragged", "fp32", "ternary-fp32"])
     ap.add_argument("--workload", default="nanogpt",
                     choices=["nanogpt", "llama_vote", "vote_100m", "ns_sweep", "ns_sweep_full", "resnet50",
-                             "ternary_vote", "variants", "collectives", "cublas", "all"],
+                             "ternary_vote", "variants", "collectives", "cublas", "layers", "all"],
                     help="nanogpt: the headline line; the others print secondary measurements only")
     args = ap.parse_args()
     if args.capture_layers > 0:
