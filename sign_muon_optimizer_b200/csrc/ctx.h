@@ -88,7 +88,7 @@ struct signmuon_ctx {
   // workspace of the layer calls (signmuon_layers.h), as reserved
   int64_t lay_rows = 0, lay_cols = 0;
   uint8_t* lay_ws = nullptr;
-  int* lay_status = nullptr;    // [0] an index was out of range; then one row counter per worker, zero between calls
+  int* lay_status = nullptr;    // [0] an index was out of range; then two counters per worker, zero between calls
   int* h_lay_status = nullptr;  // pinned mirror of [0]
   std::vector<void*> allocs;
   int64_t bytes = 0;

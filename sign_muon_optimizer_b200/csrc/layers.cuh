@@ -332,6 +332,7 @@ struct NormGradArgs {
   int type;
   int64_t off_gamma, off_beta; // off_beta < 0: none
   int accumulate;
+  int* arrived;                // workspace: M counters, zero between calls
   float* part;                 // workspace: 2 x E floats per block
   int max_blocks;              // blocks that part has room for, at least M
 };
@@ -353,7 +354,7 @@ struct DistillArgs {
   float* row_loss;             // the caller's, or workspace
   void* dZ;
   int64_t ldd;
-  int* count;                  // workspace: M counters, zero between calls
+  int* count;                  // workspace: twice kMaxWorkers counters, zero between calls
   void* scratch;               // workspace: 12 bytes per row
   int* status;
 };

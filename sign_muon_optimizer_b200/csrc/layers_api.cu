@@ -145,9 +145,9 @@ int signmuon_layers_reserve(signmuon_t h, int64_t max_rows, int64_t max_cols) {
     TRY(dalloc(h, &ws, n));
     if (h->lay_status == nullptr) {
       int* p = nullptr;
-      TRY(dalloc(h, &p, 1 + sm::kMaxWorkers));
+      TRY(dalloc(h, &p, 1 + 2 * sm::kMaxWorkers));
       CK(h, cudaMallocHost(&h->h_lay_status, sizeof(int)));
-      CK(h, cudaMemsetAsync(p, 0, (1 + sm::kMaxWorkers) * sizeof(int), h->stream));
+      CK(h, cudaMemsetAsync(p, 0, (1 + 2 * sm::kMaxWorkers) * sizeof(int), h->stream));
       CK(h, cudaStreamSynchronize(h->stream));
       h->lay_status = p;
     }
@@ -310,6 +310,7 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
     a.off_gamma = h->plan.mats[gamma].off;
     a.off_beta = beta < 0 ? -1 : h->plan.mats[beta].off;
     a.accumulate = accumulate != 0;
+    a.arrived = h->lay_status + 1 + sm::kMaxWorkers;
     a.part = reinterpret_cast<float*>(h->lay_ws);
     a.max_blocks = norm_blocks(h);
     NvtxRange range("signmuon layernorm_grad");

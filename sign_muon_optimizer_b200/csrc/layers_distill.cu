@@ -397,18 +397,20 @@ constexpr int kBlocks = 5;      // of 256 threads on an SM
 // the registers that this leaves are enough (fp16's conversions take more)
 template <typename T, int ROW_THREADS>
 constexpr int min_blocks() {
-  return ROW_THREADS == 32 ? 9 : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
+  return ROW_THREADS == 32 ? (Elem<T>::kHalf ? 8 : 9) : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
 }
 constexpr int kAhead = 2;       // packs a thread loads before it uses the first
-template <typename T, int ROW_THREADS, bool GRAD>
-__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blocks<T, ROW_THREADS>())
+template <typename T, int ROW_THREADS, bool GRAD, bool FEW>
+__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 4 : min_blocks<T, ROW_THREADS>())
     k_distill_rows(const RowMap map, const Teacher te, const RowStat* stat, const int* kinds,
-                   const T* Z, int64_t ldz, int V, float temperature, float gscale, const int* count,
-                   float* __restrict__ row_loss, T* dZ, int64_t ldd, int early, int hold) {
+                   const T* Z, int64_t ldz, int V, float temperature, float gscale, int* count, float* row_loss, T* dZ,
+                   int64_t ldd, int early, int hold, int* arrived, float* loss_out, int32_t* count_out) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1, WARPS = ROW_THREADS / 32;
   extern __shared__ uint4 shared[];               // `hold` packs; per row: 3 arrays of K
   __shared__ float2 buf[WARPS];
   __shared__ float losses[WARPS];
+  __shared__ double sums[WARPS];
+  __shared__ int is_last;
   const bool first = (int)blockIdx.x < early;
   if (!first) griddep_wait();
   griddep_launch();
@@ -426,6 +428,48 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blo
     if (first) griddep_wait();
     return;
   }
+  const int m = worker_of(map.start, map.M, r);
+  // With FEW rows, the one that is done last adds up its worker's losses, in
+  // order, and leaves both of the worker's counters at zero.
+  auto finish = [&] {
+    if (!FEW) return;
+    if (blockIdx.x == 0 && in_block == 0)
+      for (int i = tid; i < map.M; i += ROW_THREADS)
+        if (map.start[i] == map.start[i + 1]) {
+          loss_out[i] = 0.f;
+          if (count_out != nullptr) count_out[i] = 0;
+        }
+    int last = 0;
+    if (tid == 0) {
+      __threadfence();
+      last = atomicAdd(&arrived[m], 1) == map.start[m + 1] - map.start[m] - 1;
+    }
+    if (ROW_THREADS == 32) {
+      last = __shfl_sync(0xffffffffu, last, 0);
+    } else {
+      if (tid == 0) is_last = last;
+      __syncthreads();
+      last = is_last;
+    }
+    if (!last) return;
+    __threadfence();
+    double t = 0.0;
+    for (int i = map.start[m] + tid; i < map.start[m + 1]; i += ROW_THREADS) t += (double)__ldcg(row_loss + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (ROW_THREADS > 32) {
+      if ((tid & 31) == 0) sums[tid >> 5] = t;
+      __syncthreads();
+      t = 0.0;
+      for (int i = 0; i < WARPS; ++i) t += sums[i];
+    }
+    if (tid == 0) {
+      const int n = count[m];
+      count[m] = arrived[m] = 0;
+      loss_out[m] = n > 0 ? (float)(t / n) : 0.f;
+      if (count_out != nullptr) count_out[m] = n;
+    }
+  };
   T* dz = GRAD ? dZ + (int64_t)r * ldd : nullptr;
   int kind = first ? (int)ROW_ONCE : kinds[r];
   const RowView<T> v(Z + (int64_t)r * ldz, V);
@@ -451,6 +495,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blo
   if (kind == ROW_NONE) {
     if (GRAD) zero_row(dz, V, tid, ROW_THREADS);
     if (tid == 0) row_loss[r] = 0.f;
+    finish();
     return;
   }
   float loss = 0.f;
@@ -469,7 +514,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blo
   }
   if (WARPS > 1 && (tid & 31) == 0) losses[tid >> 5] = loss;
   if (GRAD) {
-    const float w = gscale * temperature / (float)count[worker_of(map.start, map.M, r)], ws = w / x.s;
+    const float w = gscale * temperature / (float)count[m], ws = w / x.s;
     if (x.far) {
       for (int i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
     } else {
@@ -490,6 +535,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, min_blo
     }
     row_loss[r] = loss * (temperature * temperature);
   }
+  finish();
 }
 
 // loss[m], count[m]; leaves the counters at zero for the next call
@@ -520,13 +566,16 @@ struct Scratch {
   int* kind;
 };
 
+// Calls of so few rows add up the losses in the rows' kernel: that saves a
+// launch, but the rows end a round trip to L2 later.
+constexpr int kFewRows = 1024;
 constexpr int64_t kL2Bytes = 50'000'000;
 
-template <typename T, int ROW_THREADS, bool GRAD>
+template <typename T, int ROW_THREADS, bool GRAD, bool FEW>
 void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   constexpr int ROWS = ROW_THREADS == 32 ? 4 : 1;
   size_t smem = (size_t)ROWS * 3 * a.K * 4;
-  auto* kernel = k_distill_rows<T, ROW_THREADS, GRAD>;
+  auto* kernel = k_distill_rows<T, ROW_THREADS, GRAD, FEW>;
   int hold = 0;
   if (GRAD && ROW_THREADS == 256) {
     // What the rows on their way have in L2 must stay within half of it, or the
@@ -549,19 +598,19 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
   count_launch();
   launch_pdl(kernel, dim3(blocks), dim3(ROWS * ROW_THREADS), smem, s, map, te, (const RowStat*)x.stat,
              (const int*)x.kind, reinterpret_cast<const T*>(a.Z), a.ldz, (int)a.V, a.temperature, a.gscale,
-             (const int*)a.count, a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd, early,
-             hold);
+             a.count, a.row_loss, reinterpret_cast<T*>(a.dZ), a.ldd, early, hold,
+             a.count + kMaxWorkers, a.loss, a.count_out);
 }
 
 // Few threads for short rows, so that each has something to load: 16384 rows
 // with gradient of 4000 bf16 take 71 / 91 / 135 us with 32 / 128 / 256 threads,
 // of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382.
-template <typename T, bool GRAD>
+template <typename T, bool GRAD, bool FEW>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   const int64_t row = a.V * (int64_t)sizeof(T);
-  if (row <= 16 * 1024) run_rows<T, 32, GRAD>(s, a, map, te, x);
-  else if (row <= 48 * 1024) run_rows<T, 128, GRAD>(s, a, map, te, x);
-  else run_rows<T, 256, GRAD>(s, a, map, te, x);
+  if (row <= 16 * 1024) run_rows<T, 32, GRAD, FEW>(s, a, map, te, x);
+  else if (row <= 48 * 1024) run_rows<T, 128, GRAD, FEW>(s, a, map, te, x);
+  else run_rows<T, 256, GRAD, FEW>(s, a, map, te, x);
 }
 
 }  // namespace
@@ -582,12 +631,15 @@ void launch_distill(cudaStream_t s, const DistillArgs& a, const int* start, int 
     else
       launch_pdl(k_distill_teacher<256>, dim3(N), dim3(256), 0, s, map, te, a.V, inv_T, x.stat, x.kind, a.count,
                  a.status);
-#define SM_PICK(T) (a.dZ != nullptr ? pick_rows<T, true>(s, a, map, te, x) : pick_rows<T, false>(s, a, map, te, x))
+#define SM_FEW(T, GRAD) (N <= kFewRows ? pick_rows<T, GRAD, true>(s, a, map, te, x) : pick_rows<T, GRAD, false>(s, a, map, te, x))
+#define SM_PICK(T) (a.dZ != nullptr ? SM_FEW(T, true) : SM_FEW(T, false))
     if (a.type == LT_F32) SM_PICK(float);
     else if (a.type == LT_BF16) SM_PICK(__nv_bfloat16);
     else SM_PICK(__half);
 #undef SM_PICK
+#undef SM_FEW
   }
+  if (N > 0 && N <= kFewRows) return;
   count_launch();
   launch_pdl(k_distill_loss, dim3(M), dim3(256), 0, s, map, (const float*)a.row_loss, a.count, a.loss, a.count_out);
 }

@@ -4,14 +4,15 @@
 namespace sm {
 namespace {
 
-constexpr int kStages = 3;
+// rows on their way: four where two blocks' slots still fit an SM
+constexpr int stages(int strips, int threads) { return strips * threads * 16 * 4 * 2 <= 226 * 1024 ? 4 : 3; }
 
 // ---------------------------------------------------------------------------
 // Y = (X - mean) * rstd * gamma + beta.  Bound by the bytes (X read once, Y
 // written once).  WPR warps hold a row in registers, EPL elements a lane, so
 // the variance is summed around the mean without a second read; gamma and
 // beta stay in registers too where there is room.  Rows on 16-byte boundaries come in through
-// asynchronous copies, kStages rows ahead, into slots that only the copying
+// asynchronous copies, three or four rows ahead, into slots that only the copying
 // thread reads.
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC, int WPR, int EPL>
@@ -24,6 +25,7 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256)
   constexpr int WARPS = WPR > 8 ? WPR : 8;
   constexpr int RPB = WARPS / WPR;                  // rows per block
   constexpr bool KEEP = VEC || EPL <= 24;           // gamma and beta in registers, where there is room
+  constexpr int kStages = stages(CH, WARPS * 32);
   extern __shared__ uint4 ring[];                   // VEC: [kStages][CH][threads]
   __shared__ float buf[2][WARPS];
   griddep_wait();
@@ -154,7 +156,8 @@ struct FwdArgs {
 template <typename T, bool VEC, int WPR, int EPL>
 void run_fwd(cudaStream_t s, const FwdArgs& a) {
   constexpr int WARPS = WPR > 8 ? WPR : 8;
-  const size_t smem = VEC ? (size_t)kStages * (EPL / Elem<T>::V) * WARPS * 32 * 16 : 0;
+  constexpr int CH = EPL / Elem<T>::V;
+  const size_t smem = VEC ? (size_t)stages(CH, WARPS * 32) * CH * WARPS * 32 * 16 : 0;
   auto* kernel = k_ln_fwd<T, VEC, WPR, EPL>;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   const int grid = stream_grid((const void*)kernel, WARPS * 32, smem, (a.n + WARPS / WPR - 1) / (WARPS / WPR), 8);

@@ -21,11 +21,12 @@ constexpr int kStages = 3;
 // and no shared memory for the slots: their sums are in shared memory, and the
 // second pass loads them again (from L2).
 // ---------------------------------------------------------------------------
-template <typename T, bool VEC, int WPR, int EPL>
+template <typename T, bool VEC, int WPR, int EPL, bool FEW>
 __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
     k_ln_bwd(const RowMap map, int rows_per_unit, const T* X, int64_t ldx, const T* dY, int64_t ldy,
              const float* gamma, const float* mean, const float* rstd, T* dX,
-             int64_t ldd, int E, float* __restrict__ part) {
+             int64_t ldd, int E, float* part, int* arrived, const GradPtrs G, int64_t off_gamma, int64_t off_beta,
+             int accumulate) {
   constexpr int VL = Elem<T>::V;
   constexpr int CH = EPL / VL;                      // strips per warp
   constexpr int WARPS = WPR > 8 ? WPR : 8;
@@ -199,10 +200,9 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
       out[col] = sums[col];
       out[E + col] = sums[COLS + col];
     }
-    return;
   }
   if (RING) copy_wait<0>();
-  for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < (WIDE ? 0 : 2); ++which) {
     if (RPB > 1) __syncthreads();
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -224,6 +224,29 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
         for (int i = 0; i < RPB; ++i) t += sums[i * COLS + col];
         out[which * E + col] = t;
       }
+    }
+  }
+  if (!FEW) return;
+  // few blocks: the one of the worker that is done last adds up their sums
+  __shared__ int is_last;
+  const int units = map.unit[m + 1] - map.unit[m];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    is_last = atomicAdd(&arrived[m], 1) == units - 1;
+    if (is_last) arrived[m] = 0;
+  }
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  const float* from = part + (int64_t)map.unit[m] * 2 * E;
+  for (int which = 0; which < (off_beta >= 0 ? 2 : 1); ++which) {
+    float* g = G.p[m] + (which ? off_beta : off_gamma);
+    for (int col = threadIdx.x; col < E; col += WARPS * 32) {
+      float t = 0.f;
+#pragma unroll 4
+      for (int u = 0; u < units; ++u) t += __ldcg(from + ((int64_t)u * 2 + which) * E + col);
+      g[col] = accumulate ? g[col] + t : t;
     }
   }
 }
@@ -258,10 +281,15 @@ __global__ void __launch_bounds__(256) k_ln_weights(const RowMap map, const Grad
   }
 }
 
+// Where every worker has at most kFewRows rows they go in at most kFewUnits
+// units, and the sums over those are made in the same launch (by one block,
+// while the separate kernel takes E / 32): that saves a launch.
+constexpr int kFewUnits = 16, kFewRows = 128;
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, bool VEC, int WPR, int EPL>
-void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+template <typename T, bool VEC, int WPR, int EPL, bool FEW>
+void run_units(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
   constexpr int WARPS = WPR > 8 ? WPR : 8;
   constexpr int RPB = WARPS / WPR;
   constexpr int COLS = WPR * 32 * EPL;
@@ -269,7 +297,7 @@ void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, con
   const size_t ring = VEC && !WIDE ? (size_t)kStages * 2 * (EPL / Elem<T>::V) * WARPS * 32 * 16 : 0;
   const size_t sums = WIDE ? (size_t)2 * COLS * 4 : (RPB > 1 ? (size_t)RPB * COLS * 4 : 0);
   const size_t smem = ring > sums ? ring : sums;
-  auto* kernel = k_ln_bwd<T, VEC, WPR, EPL>;
+  auto* kernel = k_ln_bwd<T, VEC, WPR, EPL, FEW>;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   const int N = start[M];
   // one wave of blocks; every worker's rows split into units of equal length
@@ -277,21 +305,39 @@ void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, con
   if (want > a.max_blocks - M) want = a.max_blocks - M;
   if (want < 1) want = 1;
   int64_t per = (N + want - 1) / want;
+  if (FEW) {
+    int longest = 0;
+    for (int m = 0; m < M; ++m) longest = longest > start[m + 1] - start[m] ? longest : start[m + 1] - start[m];
+    const int64_t least = (longest + kFewUnits - 1) / kFewUnits;
+    if (per < least) per = least;
+  }
   per = (per + RPB - 1) / RPB * RPB;
   if (per < RPB) per = RPB;
   RowMap map{};
   map.M = M;
   for (int m = 0; m <= M; ++m) map.start[m] = start[m];
-  for (int m = 0; m < M; ++m) map.unit[m + 1] = map.unit[m] + (int)((start[m + 1] - start[m] + per - 1) / per);
+  for (int m = 0; m < M; ++m) {
+    const int units = (int)((start[m + 1] - start[m] + per - 1) / per);
+    map.unit[m + 1] = map.unit[m] + (FEW && units == 0 ? 1 : units);   // (FEW: one that writes the zeros)
+  }
   if (map.unit[M] > 0) {
     count_launch();
     launch_pdl(kernel, dim3(map.unit[M]), dim3(WARPS * 32), smem, s, map, (int)per, reinterpret_cast<const T*>(a.X),
                a.ldx, reinterpret_cast<const T*>(a.dY), a.ldy, a.gamma, a.mean, a.rstd, reinterpret_cast<T*>(a.dX),
-               a.ldd, (int)a.E, a.part);
+               a.ldd, (int)a.E, a.part, a.arrived, G, a.off_gamma, a.off_beta, a.accumulate);
   }
+  if (FEW) return;
   count_launch();
   launch_pdl(k_ln_weights, dim3((unsigned)((a.E + 31) / 32), M, a.off_beta >= 0 ? 2 : 1), dim3(256), 0, s, map, G,
              (const float*)a.part, (int)a.E, a.off_gamma, a.off_beta, a.accumulate);
+}
+
+template <typename T, bool VEC, int WPR, int EPL>
+void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+  bool few = true;
+  for (int m = 0; m < M; ++m) few = few && start[m + 1] - start[m] <= kFewRows;
+  if (few) run_units<T, VEC, WPR, EPL, true>(s, a, start, M, G);
+  else run_units<T, VEC, WPR, EPL, false>(s, a, start, M, G);
 }
 
 // the fewest warps that hold a row at 16 elements a lane; beyond 16 warps, 32

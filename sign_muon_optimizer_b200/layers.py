@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from operator import attrgetter
 
 SIGNMUON_F32 = 0
 SIGNMUON_BF16 = 1
@@ -31,11 +32,13 @@ __all__ = EXPORTED_LAYERS + [
 
 _types = {}     # torch dtype -> type code, filled with the first tensor: the package itself does not import torch
 _id_types = {}
+_dtype_of = attrgetter("dtype")
 
 
 def _fill_types():
     import torch
-    _types.update({torch.float32: SIGNMUON_F32, torch.bfloat16: SIGNMUON_BF16, torch.float16: SIGNMUON_F16})
+    _types.update({torch.float32: SIGNMUON_F32, torch.bfloat16: SIGNMUON_BF16, torch.float16: SIGNMUON_F16,
+                   "Tensor": torch.Tensor, "float32": {torch.float32}})
     _id_types.update({torch.int32: SIGNMUON_I32, torch.int64: SIGNMUON_I64})
 
 
@@ -193,12 +196,14 @@ def _grads(opt, G):
         raise ValueError(f"G has {len(G)} vectors, wanted one for each of {opt.M} workers")
     if not _types:
         _fill_types()
-    device, d, at = opt.device, opt.d, []
-    for g in G:
-        if _device_of(g) != device or _types.get(g.dtype) != SIGNMUON_F32 or g.numel() < d or not g.is_contiguous():
-            _vector(opt, "G[m]", g, d)   # says which
-        at.append(g.data_ptr())
-    return array("Q", at)
+    T = _types["Tensor"]
+    try:
+        if (set(map(T.get_device, G)) == {opt.device} and set(map(_dtype_of, G)) == _types["float32"]
+                and min(map(T.numel, G)) >= opt.d and all(map(T.is_contiguous, G))):
+            return array("Q", map(T.data_ptr, G))
+    except TypeError:                    # not a tensor
+        pass
+    return array("Q", [_vector(opt, "G[m]", g, opt.d) for g in G])   # says which, and what is wrong
 
 
 def _mat(opt, name, mat):
