@@ -394,14 +394,15 @@ __device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
 // is) and wait for it where they need its results; behind them rows without
 // entries are known before their logits are read.
 constexpr int kBlocks = 5;      // of 256 threads on an SM
-// the registers that this leaves are enough (fp16's conversions take more)
+// the registers that this leaves are enough (fp16's conversions take more; the
+// 512-thread gradient keeps a few bytes elsewhere, for a third block)
 template <typename T, int ROW_THREADS>
 constexpr int min_blocks() {
-  return ROW_THREADS == 32 ? (Elem<T>::kHalf ? 8 : 9) : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
+  return ROW_THREADS == 512 ? 3 : ROW_THREADS == 32 ? (Elem<T>::kHalf ? 8 : 9) : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
 }
 constexpr int kAhead = 2;       // packs a thread loads before it uses the first
 template <typename T, int ROW_THREADS, bool GRAD, bool FEW>
-__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 4 : min_blocks<T, ROW_THREADS>())
+__global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 2 : min_blocks<T, ROW_THREADS>())
     k_distill_rows(const RowMap map, const Teacher te, const RowStat* stat, const int* kinds,
                    const T* Z, int64_t ldz, int V, float temperature, float gscale, int* count, float* row_loss, T* dZ,
                    int64_t ldd, int early, int hold, int* arrived, float* loss_out, int32_t* count_out) {
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 4
   __shared__ float2 buf[WARPS];
   __shared__ float losses[WARPS];
   __shared__ double sums[WARPS];
+  __shared__ float4 kept[ROWS];
   __shared__ int is_last;
   const bool first = (int)blockIdx.x < early;
   if (!first) griddep_wait();
@@ -515,6 +517,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 4
   if (WARPS > 1 && (tid & 31) == 0) losses[tid >> 5] = loss;
   if (GRAD) {
     const float w = gscale * temperature / (float)count[m], ws = w / x.s;
+    if (tid == 0) kept[in_block] = make_float4(x.all, x.s, w, kind == ROW_TWICE ? 1.f : 0.f);
     if (x.far) {
       for (int i = tid; i < V; i += ROW_THREADS) dz[i] = x.grad(Elem<T>::up(v.z[i]), w);
     } else {
@@ -523,8 +526,12 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 4
       if (tid < v.head) dz[tid] = x.grad(Elem<T>::up(v.z[tid]), w);
       if (v.tail() + tid < V) dz[v.tail() + tid] = x.grad(Elem<T>::up(v.z[v.tail() + tid]), w);
     }
+    // (what is needed behind the gradient waits in shared memory: its loop has
+    // no registers to spare)
     sync();
-    for (int k = tid; k < K; k += ROW_THREADS) correct(e, K, k, kind == ROW_TWICE, x, w, dz);
+    const float4 was = kept[in_block];
+    const Softmax<T> y(was.x, was.y, c);
+    for (int k = tid; k < K; k += ROW_THREADS) correct(e, K, k, was.w != 0.f, y, was.z, dz);
   } else {
     sync();
   }
@@ -577,18 +584,18 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
   size_t smem = (size_t)ROWS * 3 * a.K * 4;
   auto* kernel = k_distill_rows<T, ROW_THREADS, GRAD, FEW>;
   int hold = 0;
-  if (GRAD && ROW_THREADS == 256) {
+  if (GRAD && ROW_THREADS >= 256) {
     // What the rows on their way have in L2 must stay within half of it, or the
-    // second reading misses it: where kBlocks rows an SM are too much, their
-    // first packs are held in shared memory (8192 x 50304 bf16: 369 -> 351 us),
-    // and the longest rows go with fewer blocks.
+    // second reading misses it: where it would not, the rows' first packs are
+    // held in shared memory, and the longest rows go with fewer blocks.
+    constexpr int BATCH = ROW_THREADS * kAhead;
     const int64_t row = a.V * (int64_t)sizeof(T);
-    for (int blocks = kBlocks; blocks >= 1; --blocks) {
-      const int64_t room = (int64_t)226 * 1024 / blocks - 1536 - (int64_t)smem;
-      const int64_t fits = row / 16 / (ROW_THREADS * kAhead) * (ROW_THREADS * kAhead), can = room / 16 / (ROW_THREADS * kAhead) * (ROW_THREADS * kAhead);
-      if (blocks == kBlocks && num_sms() * blocks * row <= kL2Bytes) break;
-      hold = (int)(can < 0 ? 0 : can < fits ? can : fits);
-      if (blocks == 1 || num_sms() * blocks * (row - hold * (int64_t)16) <= kL2Bytes) break;
+    int blocks = min_blocks<T, ROW_THREADS>();
+    if (num_sms() * blocks * row <= kL2Bytes) blocks = 0;
+    for (; blocks >= 1; --blocks) {
+      const int64_t room = ((int64_t)226 * 1024 / blocks - 1536 - (int64_t)smem) / 16, packs = row / 16;
+      hold = (int)((room < 0 ? 0 : room < packs ? room : packs) / BATCH * BATCH);
+      if (num_sms() * blocks * (row - hold * (int64_t)16) <= kL2Bytes) break;
     }
     smem += (size_t)hold * 16;
   }
@@ -604,13 +611,16 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
 
 // Few threads for short rows, so that each has something to load: 16384 rows
 // with gradient of 4000 bf16 take 71 / 91 / 135 us with 32 / 128 / 256 threads,
-// of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382.
+// of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382; 8192 rows of
+// 50304 bf16 350 with 256 and 324 with 512, of 32003 214 and 238, for which
+// L2 is large enough either way.
 template <typename T, bool GRAD, bool FEW>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   const int64_t row = a.V * (int64_t)sizeof(T);
   if (row <= 16 * 1024) run_rows<T, 32, GRAD, FEW>(s, a, map, te, x);
   else if (row <= 48 * 1024) run_rows<T, 128, GRAD, FEW>(s, a, map, te, x);
-  else run_rows<T, 256, GRAD, FEW>(s, a, map, te, x);
+  else if (row <= 80 * 1024) run_rows<T, 256, GRAD, FEW>(s, a, map, te, x);
+  else run_rows<T, GRAD ? 512 : 256, GRAD, FEW>(s, a, map, te, x);
 }
 
 }  // namespace
