@@ -162,4 +162,4 @@ def test_no_layer_kernel_spills_or_keeps_a_stack_frame(tmp_path):
     # the 512-thread distillation kernels may keep a few bytes: 40 registers let
     # a third block onto an SM, which is worth 324 against 376 us
     assert not {name: frame for name, frame in found.items()
-                if frame != (0, 0, 0) and not ("k_distill_rows" in name and "Li512ELb1ELb0E" in name and max(frame) <= 40)}
+                if frame != (0, 0, 0) and not ("k_distill_rows" in name and "Li512ELb1ELb0E" in name and frame[0] <= 16)}
