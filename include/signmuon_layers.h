@@ -24,6 +24,7 @@
  *   - The calls use one workspace per handle: calls, and replays of graphs
  *     that hold them, must not overlap each other on different streams.
  *   - Sums have a fixed order: equal inputs give equal bits.
+ *   - The M vectors of G are written by these calls and must not overlap.
  *   - Outputs must not overlap inputs, except where a call says so.
  */
 #ifndef SIGNMUON_LAYERS_H
@@ -138,7 +139,7 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
  *   row_loss  device float[rows], may be NULL.
  *   dZ     rows x V of `type`, row stride ldd; may be Z itself (same pointer
  *          and row stride).
- * temperature > 0, 1 <= V <= 2^30, 1 <= K <= SIGNMUON_DISTILL_MAX_K (E_UNSUPPORTED).
+ * 1e-18 <= temperature <= 1e18, 1 <= V <= 2^30, 1 <= K <= SIGNMUON_DISTILL_MAX_K (E_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t V, const void* idx,
                      int id_type, const void* t, int t_type, int64_t ldt, int K,

@@ -1,5 +1,6 @@
 // layers_api.cu -- the C ABI of include/signmuon_layers.h: argument checks,
 // the workspace, and the launches on the handle's stream.
+#include <algorithm>
 #include <climits>
 #include <initializer_list>
 
@@ -90,6 +91,12 @@ int check_grads(signmuon_t h, float* const* G, sm::GradPtrs* out) {
     if (G[m] == nullptr || !aligned16(G[m])) return fail(h, SIGNMUON_E_INVALID, "G[m] null or misaligned");
     out->p[m] = G[m];
   }
+  // outputs of different workers: no two may share memory
+  float* sorted[sm::kMaxWorkers];
+  std::copy(G, G + h->M, sorted);
+  std::sort(sorted, sorted + h->M);
+  for (int m = 1; m < h->M; ++m)
+    if (sorted[m] - sorted[m - 1] < h->plan.d) return fail(h, SIGNMUON_E_INVALID, "two gradient vectors overlap");
   return SIGNMUON_OK;
 }
 
@@ -146,7 +153,7 @@ int signmuon_layers_reserve(signmuon_t h, int64_t max_rows, int64_t max_cols) {
     if (h->lay_status == nullptr) {
       int* p = nullptr;
       TRY(dalloc(h, &p, 1 + 2 * sm::kMaxWorkers));
-      CK(h, cudaMallocHost(&h->h_lay_status, sizeof(int)));
+      if (h->h_lay_status == nullptr) CK(h, cudaMallocHost(&h->h_lay_status, sizeof(int)));
       CK(h, cudaMemsetAsync(p, 0, (1 + 2 * sm::kMaxWorkers) * sizeof(int), h->stream));
       CK(h, cudaStreamSynchronize(h->stream));
       h->lay_status = p;
@@ -332,8 +339,8 @@ int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t
     if (K < 1) return fail(h, SIGNMUON_E_INVALID, "K must be >= 1");
     if (K > SIGNMUON_DISTILL_MAX_K)
       return fail(h, SIGNMUON_E_UNSUPPORTED, "at most " + std::to_string(SIGNMUON_DISTILL_MAX_K) + " teacher entries a row");
-    if (!(temperature > 0.f) || !(1.f / temperature > 0.f) || 1.f / temperature > 3e38f)
-      return fail(h, SIGNMUON_E_INVALID, "temperature must be positive and finite, and so its inverse");
+    if (!(temperature >= 1e-18f && temperature <= 1e18f))   // its square and its inverse times log2 e stay in range
+      return fail(h, SIGNMUON_E_INVALID, "temperature must be in [1e-18, 1e18]");
     int start[sm::kMaxWorkers + 1];
     TRY(check_rows(h, rows, start));
     const int64_t n = start[h->M];

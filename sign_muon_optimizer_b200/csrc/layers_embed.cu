@@ -53,11 +53,11 @@ __global__ void __launch_bounds__(256) k_embed(const float* table, int64_t V, in
 // the bytes: dY read once, M dense tables written once.
 //
 // The tokens of each worker are sorted by (id, row): up to kSortTile of them in
-// registers, more by a radix sort.  A block then takes a unit of sorted tokens of one worker and a strip
-// of columns, a warp an eighth of them, one key per lane, and adds up their dY
-// rows in registers; parts of a run of equal ids are added up in order across
-// the warps through shared memory, and where it goes on in other blocks by
-// k_embed_join.  Work per block does not depend on how often a token occurs,
+// registers, more by a radix sort.  A block then takes a unit of sorted tokens
+// of one worker and a strip of columns, a warp an eighth of them, one key per
+// lane, and adds up their dY rows in registers; parts of a run of equal ids are
+// added up in order across the warps through shared memory, and where it goes on
+// in other blocks by k_embed_join.  Work per block does not depend on how often a token occurs,
 // and every sum has a fixed order.  Further blocks of the same launch write
 // zeros to the rows without tokens, so that every byte of G is written once.
 // Absent tokens (id < 0, id >= V) get the id kAbsent and sort to the end.
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, c
 // tiles' digit counts; a token's place behind that comes from counting in order:
 // warps take 32 tokens at a time and match equal digits.
 // The first counts are made by k_radix_count; each scatter makes the next
-// digit's by (integer) atomics.  There is a set of counts per digit.  Absent tokens sort as id V.
+// digit's by (integer) atomics.  There is a set of counts per digit.  Absent
+// tokens sort as id V.
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 static_assert(kBins == kRadixBins && kRadixSets * kDigitBits >= 31, "the workspace has a set of counts per digit");
 

@@ -246,8 +246,11 @@ def test_reserve_and_refusals_of_a_handle():
     refused(I, opt.embed, W[1:1 + opt.d] if W.numel() > opt.d else torch.zeros(opt.d + 1, device="cuda")[1:], 0, ids, X)
     refused(I, opt.embed_grad, 0, ids, X, [g[1:] for g in G])  # misaligned vectors
     refused(I, opt.embed_grad, 0, ids, X, G, rows=[7, -1])
+    both = torch.zeros(2 * opt.d, device="cuda")
+    refused(I, opt.embed_grad, 0, ids, X, [G[0], G[0]])        # two workers' gradients in the same place
+    refused(I, opt.embed_grad, 0, ids, X, [both, both[opt.d // 4 * 4 - 4:][:opt.d]])
     loss, t, idx = torch.zeros(2, device="cuda"), torch.zeros(6, 2, device="cuda"), torch.zeros(6, 2, dtype=torch.int32, device="cuda")
-    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-45):
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-45, 1e-19, 1e19):
         refused(I, opt.distill, X, idx, t, loss, temperature=bad)
     refused(U, opt.distill, X, torch.zeros(6, 1025, dtype=torch.int32, device="cuda"), torch.zeros(6, 1025, device="cuda"), loss)
     big = torch.zeros(12, 8, device="cuda")
