@@ -22,7 +22,7 @@ constexpr int kStages = 3;
 // second pass loads them again (from L2).
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC, int WPR, int EPL, bool FEW>
-__global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, WPR > 8 ? 1 : 2)
+__global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, (WPR > 8 ? 1 : 2) + (EPL <= 8 ? 1 : 0))
     k_ln_bwd(const RowMap map, int rows_per_unit, const T* X, int64_t ldx, const T* dY, int64_t ldy,
              const float* gamma, const float* mean, const float* rstd, T* dX,
              int64_t ldd, int E, float* part, int* arrived, const GradPtrs G, int64_t off_gamma, int64_t off_beta,
@@ -340,14 +340,19 @@ void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, con
   else run_units<T, VEC, WPR, EPL, false>(s, a, start, M, G);
 }
 
-// the fewest warps that hold a row at 16 elements a lane; beyond 16 warps, 32
+// The fewest warps that hold a row at 16 elements a lane; without the
+// asynchronous copies at 8, which lets a third block wait on its loads too
+// (30000 x 1001 fp32 86 us instead of 107, 8000 x 4001 bf16 68 instead of 80;
+// with the copies 32768 x 4096 bf16 takes 216 us at 8 and 153 at 16).  Above
+// 16 warps at 16, 32.
 template <typename T, bool VEC>
 void pick_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
+  constexpr int MORE = VEC ? 1 : 2, EPL = 16 / MORE;
   if (a.E <= 256) run_bwd<T, VEC, 1, 8>(s, a, start, M, G);
-  else if (a.E <= 512) run_bwd<T, VEC, 1, 16>(s, a, start, M, G);
-  else if (a.E <= 1024) run_bwd<T, VEC, 2, 16>(s, a, start, M, G);
-  else if (a.E <= 2048) run_bwd<T, VEC, 4, 16>(s, a, start, M, G);
-  else if (a.E <= 4096) run_bwd<T, VEC, 8, 16>(s, a, start, M, G);
+  else if (a.E <= 512) run_bwd<T, VEC, MORE, EPL>(s, a, start, M, G);
+  else if (a.E <= 1024) run_bwd<T, VEC, 2 * MORE, EPL>(s, a, start, M, G);
+  else if (a.E <= 2048) run_bwd<T, VEC, 4 * MORE, EPL>(s, a, start, M, G);
+  else if (a.E <= 4096) run_bwd<T, VEC, 8 * MORE, EPL>(s, a, start, M, G);
   else if (a.E <= 8192) run_bwd<T, VEC, 16, 16>(s, a, start, M, G);
   else run_bwd<T, VEC, 16, 32>(s, a, start, M, G);
 }
