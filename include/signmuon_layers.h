@@ -129,8 +129,8 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
  *   loss[m] = sum over worker m's rows / count[m],
  *   dZ[r][v] = gscale * T / count[m] * (p[v] - sum of q_k with idx_k = v),
  * count[m] the worker's rows with at least one entry.  A row without entries
- * has loss 0 and a gradient of zeros, and its logits are not read; a worker
- * without such rows has loss 0.  Entries with the same idx add up.  K = 1 is
+ * has loss 0 and a gradient of zeros, whatever its logits hold; a worker
+ * without rows that count has loss 0.  Entries with the same idx add up.  K = 1 is
  * the cross-entropy with the label idx (for T = 1).  A logit of -inf is a
  * masked entry (p = 0); a row whose logits are all -inf gives NaN.
  *   Z      rows x V of `type`, row stride ldz.
@@ -139,7 +139,8 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
  *   row_loss  device float[rows], may be NULL.
  *   dZ     rows x V of `type`, row stride ldd; may be Z itself (same pointer
  *          and row stride).
- * 1e-18 <= temperature <= 1e18, 1 <= V <= 2^30, 1 <= K <= SIGNMUON_DISTILL_MAX_K (E_UNSUPPORTED).
+ * 1e-18 <= temperature <= 1e18, 1 <= V <= 2^30, 1 <= K; K <= SIGNMUON_DISTILL_MAX_K
+ * (E_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t V, const void* idx,
                      int id_type, const void* t, int t_type, int64_t ldt, int K,

@@ -348,7 +348,7 @@ int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t
     TRY(check_matrix(h, "t", t, t_type, n, K, ldt));
     TRY(check_ids(h, idx, id_type, n));
     TRY(check_floats(h, "loss", loss, h->M));
-    TRY(check_floats(h, "count", count, count ? n : 0));
+    TRY(check_floats(h, "count", count, count ? h->M : 0));
     TRY(check_floats(h, "row_loss", row_loss, row_loss ? n : 0));
     if (dZ != nullptr) {
       TRY(check_matrix(h, "dZ", dZ, type, n, V, ldd));

@@ -256,8 +256,82 @@ def test_reserve_and_refusals_of_a_handle():
     big = torch.zeros(12, 8, device="cuda")
     refused(I, opt.distill, big[::2], idx, t, loss, dZ=big.view(-1)[:48].view(6, 8))   # the same memory, another stride
     refused(I, opt.layernorm_grad, W, 1, None, X, big[::2], mean, mean, big.view(-1)[:48].view(6, 8), G)
+    # outputs per worker are written for no rows too
+    none = torch.zeros(0, 8, device="cuda"), torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 2, device="cuda")
+    ints = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for where in (1, 2, 3):
+        with pytest.raises(smo.SignMuonError):
+            smo.signmuon_distill(opt.h, none[0].data_ptr(), 0, 8, 8, none[1].data_ptr(), 0, none[2].data_ptr(), 0, 2, 2,
+                                 [0, 0], 1.0, 1.0, loss, ints.data_ptr() + where, None, None, 8)
     wide = smo.SignMuon([(1, smo.SIGNMUON_LAYERNORM_MAX_COLS + 1)], 1, flags=smo.SIGNMUON_VOTE_ONLY)
     wide.layers_reserve(1, 8)
     x = torch.zeros(1, wide.d, device="cuda")
     refused(U, wide.layernorm, torch.zeros(wide.d, device="cuda"), 0, None, x, x.clone())
     opt.layers_sync()
+
+
+def test_a_graph_keeps_its_workspace_when_more_is_reserved():
+    stream = torch.cuda.Stream()
+    p = Pass(stream=stream.cuda_stream).fill(5)
+    torch.cuda.synchronize()
+
+    def check():
+        stream.synchronize()
+        for a, b in zip(p.G, want):
+            assert torch.equal(a[:p.opt.d], b[:p.opt.d])
+            a.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    with torch.cuda.stream(stream):
+        p.gradients()
+        want = [g.clone() for g in p.G]
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        p.gradients()
+    p.opt.layers_reserve(40 * N, 3 * E)
+    for _ in range(2):
+        with torch.cuda.stream(stream):
+            graph.replay()
+            check()
+            p.gradients()                          # the same handle's calls, in the new workspace
+            check()
+    p.opt.layers_sync()
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_offsets_beyond_32_bits(shift):
+    """Three rows 2^30 elements apart, at byte offsets up to 2^32: the same bits
+    as the rows next to each other."""
+    n, v, e, ld, ld_near = 3, 90, 64, (1 << 30) + 8 + shift, 128 + shift
+    opt = smo.SignMuon([(v, e), (1, e), (1, e)], 1, flags=smo.SIGNMUON_VOTE_ONLY)
+    opt.layers_reserve(n, e)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn(opt.d, generator=g, device="cuda")
+    ids = torch.tensor([4, 89, 4], device="cuda")
+    idx, t = torch.tensor([[1, 2], [80, 3], [5, -1]], device="cuda"), torch.randn(n, 2, generator=g, device="cuda")
+    logits = torch.randn(n, v, generator=g, device="cuda").bfloat16()
+    store = [torch.empty(2 * ld + 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    results = []
+    for stride in (ld_near, ld):
+        def make(i, cols):
+            return store[i].as_strided((n, cols), (stride, 1))
+
+        a, b = make(0, e), make(1, e)
+        G = [torch.full((opt.d,), float("nan"), device="cuda")]
+        mean, rstd, loss = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(1, device="cuda")
+        opt.embed(W, 0, ids, a)
+        got = [a.clone()]
+        opt.layernorm(W, 1, 2, a, b, mean, rstd)
+        got += [b.clone(), mean, rstd]
+        opt.layernorm_grad(W, 1, 2, a, b, mean, rstd, b, G)
+        got += [b.clone()]
+        opt.embed_grad(0, ids, b, G)
+        got += [G[0]]
+        z, dz = make(0, v), make(1, v)
+        z.copy_(logits)
+        opt.distill(z, idx, t, loss, dZ=dz)
+        results.append(got + [dz.clone(), loss])
+        opt.layers_sync()
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
