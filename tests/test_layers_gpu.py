@@ -162,14 +162,14 @@ def test_embed_grad(dt, rows, V, E, kind, gap, accumulate):
 
 
 @pytest.mark.parametrize("V", [400, (1 << 18) - 1, 1 << 18, (1 << 27) + 5])
-def test_embed_grad_with_one_to_four_sort_digits(V):
+@pytest.mark.parametrize("n", [2500, 8192, 8193])      # (by a block, and by several)
+def test_embed_grad_with_one_to_four_sort_digits(V, n):
     """The sort takes the bits of 0 ... V in digits of at most 9; the ids differ
     in every one of them."""
-    n = 2500
     opt = handle([(V, 1)], 1, n, 1)
     g = gen(V)
     ids = torch.randint(0, V, (n,), generator=g, device="cuda")
-    ids[:1500] = ids[1000:].clone()   # several tokens a row
+    ids[:1500] = ids[1000:2500].clone()   # several tokens a row
     ids[::11] = -1
     ids[5], ids[6] = 0, V - 1
     dY = torch.randn(n, 1, generator=g, device="cuda")
