@@ -36,6 +36,9 @@ enum RowKind { ROW_NONE = 0, ROW_ONCE = 1, ROW_TWICE = 2 };
 // The rows' stats and kinds, and count[m] += worker m's rows of a kind other
 // than none.  A row takes G threads: a warp (K <= 128), or the block.  Repeated
 // indices are found by inserting all of them into a hash table of 2 K slots.
+// Latency bound: 8192 rows of 64 entries take 12 us, most of it behind the
+// rows' first loads, which do not wait for it; the same work at the head of each
+// row's own block cost 90 us at 128 entries, since the row then waited for it.
 template <int G>
 __global__ void __launch_bounds__(256) k_distill_teacher(const RowMap map, const Teacher te, int64_t V, float inv_T,
                                                          RowStat* __restrict__ stat, int* __restrict__ kind, int* count,
@@ -384,7 +387,10 @@ __device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
 
 // ROW_THREADS threads take a row: a block, or a warp (short rows, four a block).
 // Bound by the bytes: the row is read for the maximum and sum of the softmax,
-// and a second time, from L2, for the gradient, which is written.  What counts
+// and a second time, from L2, for the gradient, which is written.  8192 x 50304
+// bf16 with 64 entries: 336 us for the call, 310 of them here, 5.3 TB/s of
+// DRAM (818 MB read, as if the second reading were free, and 824 written); loss
+// only, 3001 x 32003 fp16, 33 entries: 46 for the call.  What counts
 // is that there are always loads on their way: several blocks on an SM, in
 // different parts of their rows, do better than rows kept in shared memory and
 // loaded a row ahead, of which two fit (8192 x 32003 bf16, 64 entries: 217 us
@@ -545,7 +551,8 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 2
   finish();
 }
 
-// loss[m], count[m]; leaves the counters at zero for the next call
+// loss[m], count[m]; leaves the counters at zero for the next call.  A block per
+// worker: 5 us, launch included.
 __global__ void __launch_bounds__(256) k_distill_loss(const RowMap map, const float* row_loss, int* count,
                                                       float* __restrict__ loss, int32_t* __restrict__ count_out) {
   __shared__ double buf[256];
@@ -574,7 +581,7 @@ struct Scratch {
 };
 
 // Calls of so few rows add up the losses in the rows' kernel: that saves a
-// launch, but the rows end a round trip to L2 later.
+// launch (about 2.5 us), but each row ends a round trip to L2 later.
 constexpr int kFewRows = 1024;
 constexpr int64_t kL2Bytes = 50'000'000;
 

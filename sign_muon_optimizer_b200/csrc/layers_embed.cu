@@ -10,7 +10,10 @@ namespace {
 // ---------------------------------------------------------------------------
 // Lookup: out[r] = fl(scale * table[ids[r]]).  Bound by the bytes: N * E
 // elements written, one 4 * E-byte table row read per token (from L2 where
-// tokens repeat).  One warp per (row, slab of kSlab columns).
+// tokens repeat).  One warp per (row, slab of kSlab columns), so that a short row
+// is one warp's few wide loads and a long one spreads.  131072 tokens of a
+// 50304 x 768 table to bf16: 59 us, 0.93 of the time its DRAM bytes need; 8
+// tokens: 2.4 us on the device, of which the launch is nearly all.
 // ---------------------------------------------------------------------------
 constexpr int kSlab = 1024;
 
@@ -50,7 +53,10 @@ __global__ void __launch_bounds__(256) k_embed(const float* table, int64_t V, in
 
 // ---------------------------------------------------------------------------
 // Gradient: G[m][v] = scale * sum of dY[r] over worker m's tokens v.  Bound by
-// the bytes: dY read once, M dense tables written once.
+// the bytes: dY read once, M dense tables written once.  131072 tokens, 8 tables
+// of 50304 x 768, bf16: 275 us, 0.80 of the bytes' time; of them 20 the sort, 247
+// the sums and zeros (5.8 TB/s), 7 the join.  9001 tokens of odd rows, 4 tables
+// of 8191 x 1001: 55 us; 20, 33 and 4 of them.
 //
 // The tokens of each worker are sorted by (id, row): up to kSortTile of them in
 // registers, more by a radix sort.  A block then takes a unit of sorted tokens
@@ -161,7 +167,10 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, c
 // tokens of one worker a block.  Within a worker digit d of tile u starts at
 // (tokens with a smaller digit) + (tokens with d in the tiles before u), from the
 // tiles' digit counts; a token's place behind that comes from counting in order:
-// warps take 32 tokens at a time and match equal digits.
+// warps take 32 tokens at a time and match equal digits.  Two digits of 8 bits
+// and the count take about 18 us for 8193 to 131072 tokens: latency, three
+// launches in a row.  One block per worker that keeps up to 8192 tokens in shared
+// memory between the digits takes 21 us for 8192, and merging sorted tiles more.
 // The first counts are made by k_radix_count; each scatter makes the next
 // digit's by (integer) atomics.  There is a set of counts per digit.  Absent
 // tokens sort as id V.
