@@ -53,19 +53,25 @@ __global__ void __launch_bounds__(256) k_embed(const float* table, int64_t V, in
 
 // ---------------------------------------------------------------------------
 // Gradient: G[m][v] = scale * sum of dY[r] over worker m's tokens v.  Bound by
-// the bytes: dY read once, M dense tables written once.  131072 tokens, 8 tables
-// of 50304 x 768, bf16: 275 us, 0.80 of the bytes' time; of them 20 the sort, 247
-// the sums and zeros (5.8 TB/s), 7 the join.  9001 tokens of odd rows, 4 tables
-// of 8191 x 1001: 55 us; 20, 33 and 4 of them.
+// the bytes: dY read once, M dense tables written once.
 //
 // The tokens of each worker are sorted by (id, row): up to kSortTile of them in
-// registers, more by a radix sort.  A block then takes a unit of sorted tokens
-// of one worker and a strip of columns, a warp an eighth of them, one key per
-// lane, and adds up their dY rows in registers; parts of a run of equal ids are
-// added up in order across the warps through shared memory, and where it goes on
-// in other blocks by k_embed_join.  Work per block does not depend on how often a token occurs,
-// and every sum has a fixed order.  Further blocks of the same launch write
-// zeros to the rows without tokens, so that every byte of G is written once.
+// registers, up to kBlockTile by a radix sort of one block, more by one of many
+// blocks.  A block then takes a unit of sorted tokens of one worker and a strip
+// of columns, a warp an eighth of them, one key per lane, and adds up their dY
+// rows in registers; parts of a run of equal ids are added up in order across the
+// warps through shared memory, and where it goes on in other blocks by
+// k_embed_join.  Work per block does not depend on how often a token occurs, and
+// every sum has a fixed order.
+//
+// A sort waits on itself most of the time, and the zeros are most of the bytes:
+// further blocks of its launches zero the tables meanwhile.  Rows with tokens
+// are then written twice; zeroing the others alone, beside the sums, writes every
+// byte once but waits for the sort: 131072 tokens, 8 tables of 50304 x 768, bf16:
+// 259 us against 275 (8192 tokens: 197 against 210); 9001 tokens, 4 tables of
+// 8191 x 1001, fp16: 45 against 55.  Where the tokens outnumber the rows it costs
+// a little (8192 tokens, 8 x 1000 x 768, fp32: 28 against 26).
+// Of the 259 us 179 are the sort and zeros (6.9 TB/s), 76 the sums and 7 the join.
 // Absent tokens (id < 0, id >= V) get the id kAbsent and sort to the end.
 // ---------------------------------------------------------------------------
 typedef unsigned long long Key;  // id in the upper 32 bits, row in the lower
@@ -79,6 +85,28 @@ __device__ __forceinline__ K shfl_xor(K v, int lanes) {
   return __shfl_xor_sync(0xffffffffu, v, lanes);
 }
 
+// Zeros for whole tables, in chunks: what a launch of the sort writes in the
+// blocks behind its own.
+struct ZeroTables {
+  int chunk;           // entries
+  int per_table;       // chunks per table
+  int64_t first;       // this launch's first chunk
+  int64_t off, size;   // of each table in G[m]
+};
+
+__device__ __forceinline__ void zero_chunk(const GradPtrs& G, const ZeroTables& z, int b) {
+  const int64_t k = z.first + b;
+  const int m = (int)(k / z.per_table);
+  const int64_t i0 = (k - (int64_t)m * z.per_table) * z.chunk;
+  const int n = (int)min((int64_t)z.chunk, z.size - i0);
+  float* g = G.p[m] + z.off + i0;
+  const int head = min(n, (int)((4 - (reinterpret_cast<uintptr_t>(g) >> 2 & 3)) & 3));
+  const int n4 = (n - head) / 4, tid = threadIdx.x, tail = head + 4 * n4 + tid;
+  if (tid < head) g[tid] = 0.f;
+  for (int i = tid; i < n4; i += blockDim.x) reinterpret_cast<float4*>(g + head)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tail < n) g[tail] = 0.f;
+}
+
 // a block per unit of `map` (kSortTile rows of one worker): bitonic sort, PER
 // keys a thread, with exchanges in registers within a thread, by shuffles
 // within a warp and through shared memory beyond.  K = unsigned: the key is
@@ -87,13 +115,18 @@ constexpr int kPlaceBits = 11;
 static_assert(kSortTile == 1 << kPlaceBits, "a place in the tile has kPlaceBits bits");
 template <typename K>
 __global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, const void* ids, int id64,
-                                                             int64_t V, Key* __restrict__ keys, int* status) {
+                                                             int64_t V, Key* __restrict__ keys, int* status,
+                                                             const GradPtrs G, const ZeroTables zero) {
   constexpr int THREADS = kSortThreads;
   constexpr int PER = kSortTile / THREADS;
   __shared__ K swap[kSortTile];
   griddep_wait();
   griddep_launch();
   const int u = blockIdx.x;
+  if (u >= map.unit[map.M]) {
+    zero_chunk(G, zero, u - map.unit[map.M]);
+    return;
+  }
   const int m = worker_of(map.unit, map.M, u);
   const int r0 = map.start[m] + (u - map.unit[m]) * kSortTile;
   const int n = min(kSortTile, map.start[m + 1] - r0);
@@ -169,8 +202,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, c
 // tiles' digit counts; a token's place behind that comes from counting in order:
 // warps take 32 tokens at a time and match equal digits.  Two digits of 8 bits
 // and the count take about 18 us for 8193 to 131072 tokens: latency, three
-// launches in a row.  One block per worker that keeps up to 8192 tokens in shared
-// memory between the digits takes 21 us for 8192, and merging sorted tiles more.
+// launches in a row.
 // The first counts are made by k_radix_count; each scatter makes the next
 // digit's by (integer) atomics.  There is a set of counts per digit.  Absent
 // tokens sort as id V.
@@ -184,11 +216,15 @@ __device__ __forceinline__ unsigned radix_id(const void* ids, int id64, int64_t 
 
 __global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const void* ids, int id64, int64_t V,
                                                      int bits, int digits, int* __restrict__ count, int64_t set,
-                                                     int* status) {
+                                                     int* status, const GradPtrs G, const ZeroTables zero) {
   __shared__ int c[kBins];
   griddep_wait();
   griddep_launch();
   const int u = blockIdx.x;
+  if (u >= map.unit[map.M]) {
+    zero_chunk(G, zero, u - map.unit[map.M]);
+    return;
+  }
   const int m = worker_of(map.unit, map.M, u);
   const int r0 = map.start[m] + (u - map.unit[m]) * kRadixTile;
   const int n = min(kRadixTile, map.start[m + 1] - r0);
@@ -209,7 +245,8 @@ __global__ void __launch_bounds__(256) k_radix_count(const RowMap map, const voi
 __global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const void* ids, int id64,
                                                        int64_t V, int shift, int bits, const Key* src,
                                                        Key* __restrict__ dst, int* __restrict__ count,
-                                                       int* __restrict__ next) {
+                                                       int* __restrict__ next, const GradPtrs G,
+                                                       const ZeroTables zero) {
   constexpr int ROUNDS = kRadixTile / 256;
   __shared__ int warp_count[8][kBins];
   __shared__ int base[kBins];
@@ -217,6 +254,10 @@ __global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const v
   griddep_wait();
   griddep_launch();
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (u >= map.unit[map.M]) {
+    zero_chunk(G, zero, u - map.unit[map.M]);
+    return;
+  }
   const int m = worker_of(map.unit, map.M, u);
   const int r0 = map.start[m] + (u - map.unit[m]) * kRadixTile;
   const int n = min(kRadixTile, map.start[m + 1] - r0);
@@ -294,50 +335,111 @@ __global__ void __launch_bounds__(256) k_radix_scatter(const RowMap map, const v
   }
 }
 
-// Zeros for the rows without tokens: group b of `rows` table rows.  A thread
-// per row looks for its id in the worker's sorted keys; then L lanes write a row.
-struct ZeroRows {
-  int M, groups;       // groups per table
-  int rows, L;
-  int64_t off, V;
-};
+// The same sort of up to kBlockTile tokens a worker by one block, which passes
+// the keys through shared memory from digit to digit: one launch.  Two digits of
+// 2049 tokens take 11 us, of 4096 14, of 8192 21, where the launches of many
+// blocks take 18; with zeros beside it, which want one launch too, it is used up
+// to 8192, else up to half of that.
+constexpr int kBlockTile = 8192, kBlockThreads = 1024;
+inline size_t block_smem(int bits) { return kBlockTile * sizeof(Key) + ((size_t)(kBlockThreads / 32) << bits) * sizeof(int); }
 
-__device__ __forceinline__ void zero_rows(const RowMap& map, const GradPtrs& G, const Key* keys, int E,
-                                          const ZeroRows& z, int b, unsigned char* empty) {
-  const int m = b / z.groups;
-  const int64_t v0 = (int64_t)(b - m * z.groups) * z.rows;
-  const int t = threadIdx.x;
-  if (t < z.rows && v0 + t < z.V) {
-    const Key want = (Key)(v0 + t) << 32;
-    int lo = map.start[m], hi = map.start[m + 1];
-    const int end = hi;
-    while (lo < hi) {
-      const int mid = lo + ((hi - lo) >> 1);
-      if (keys[mid] < want) lo = mid + 1;
-      else hi = mid;
-    }
-    empty[t] = !(lo < end && key_id(keys[lo]) == (unsigned)(v0 + t));
+__global__ void __launch_bounds__(kBlockThreads) k_radix_block(const RowMap map, const void* ids, int id64, int64_t V,
+                                                               int bits, int digits, Key* __restrict__ dst, int* status,
+                                                               const GradPtrs G, const ZeroTables zero) {
+  constexpr int ROUNDS = kBlockTile / kBlockThreads, WARPS = kBlockThreads / 32;
+  extern __shared__ uint4 shared[];
+  Key* keys = reinterpret_cast<Key*>(shared);                        // [kBlockTile]
+  int* warp_count = reinterpret_cast<int*>(keys + kBlockTile);       // [WARPS][bins]
+  __shared__ int base[kBins];
+  __shared__ int scan[kBins / 32];
+  griddep_wait();
+  griddep_launch();
+  const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (m >= map.M) {
+    zero_chunk(G, zero, m - map.M);
+    return;
   }
-  __syncthreads();
-  const int per = 256 / z.L, l = t % z.L;
-  for (int r = t / z.L; r < z.rows && v0 + r < z.V; r += per) {
-    if (!empty[r]) continue;
-    float* g = G.p[m] + z.off + (v0 + r) * E;
-    const int head = min(E, (int)((4 - (reinterpret_cast<uintptr_t>(g) >> 2 & 3)) & 3));
-    const int n4 = (E - head) / 4;
-    if (l < head) g[l] = 0.f;
-    for (int i = l; i < n4; i += z.L) reinterpret_cast<float4*>(g + head)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = head + 4 * n4 + l; i < E; i += z.L) g[i] = 0.f;
-    for (int i = l + z.L; i < head; i += z.L) g[i] = 0.f;
+  const int r0 = map.start[m], n = map.start[m + 1] - r0;
+  const int bins = 1 << bits;
+  Key key[ROUNDS];
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {   // warp w has tokens w * 32 * ROUNDS on, 32 of them a round
+    const int i = (w * ROUNDS + j) * 32 + lane;
+    key[j] = 0ull;
+    if (i < n) {
+      const int64_t id = load_id(ids, id64, r0 + i);
+      if (id >= V) *status = 1;
+      key[j] = ((Key)(id >= 0 && id < V ? id : V) << 32) | (unsigned)(r0 + i);
+    }
+  }
+  for (int digit = 0; digit < digits; ++digit) {
+    const int shift = 32 + digit * bits;
+    for (int i = tid; i < WARPS * bins; i += kBlockThreads) warp_count[i] = 0;
+    __syncthreads();
+    int* mine = warp_count + w * bins;
+    int place[ROUNDS];
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+      const bool live = (w * ROUNDS + j) * 32 + lane < n;
+      const unsigned d = live ? (unsigned)(key[j] >> shift) & (bins - 1) : (unsigned)bins;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const int lower = __popc(same & ((1u << lane) - 1));
+      place[j] = live ? mine[d] + lower : 0;
+      __syncwarp();
+      if (live && lower == 0) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // where each digit starts, and each warp's tokens within it
+    int run = 0, sum = 0;
+    if (tid < bins) {
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        const int c = warp_count[i * bins + tid];
+        warp_count[i * bins + tid] = run;
+        run += c;
+      }
+    }
+    if (tid < kBins) {
+      sum = run;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
+      }
+      if (lane == 31) scan[w] = sum;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+      for (int i = 0; i < w; ++i) sum += scan[i];
+      base[tid] = sum - run;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+      if ((w * ROUNDS + j) * 32 + lane >= n) continue;
+      const unsigned d = (unsigned)(key[j] >> shift) & (bins - 1);
+      keys[base[d] + mine[d] + place[j]] = key[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+      const int i = (w * ROUNDS + j) * 32 + lane;
+      if (i < n) key[j] = keys[i];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {
+    const int i = (w * ROUNDS + j) * 32 + lane;
+    if (i < n) dst[r0 + i] = key_id(key[j]) == (unsigned)V ? (key[j] | ((Key)kAbsent << 32)) : key[j];
   }
 }
 
 // zeros alone (no tokens at all)
-__global__ void __launch_bounds__(256) k_zero_rows(const RowMap map, const GradPtrs G, int E, const ZeroRows zero) {
-  __shared__ unsigned char empty[256];
+__global__ void __launch_bounds__(256) k_zero_tables(const GradPtrs G, const ZeroTables zero) {
   griddep_wait();
   griddep_launch();
-  zero_rows(map, G, nullptr, E, zero, blockIdx.x, empty);
+  zero_chunk(G, zero, blockIdx.x);
 }
 
 template <typename T, bool VEC>
@@ -355,14 +457,12 @@ __device__ __forceinline__ void emit(float* row, int c, int E, int lane, const f
   strip_store_f32<T, VEC>(row, c, E, lane, x);
 }
 
-// a block per (unit of 8 * per_warp sorted tokens, strip of columns); the
-// blocks behind them zero the rows without tokens
+// a block per (unit of 8 * per_warp sorted tokens, strip of columns)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const GradPtrs G, const Key* keys,
                                                       const T* dY, int64_t ld, int E, int n_strip,
                                                       int64_t off, float scale, int accumulate,
-                                                      float* __restrict__ part, int per_warp, int every,
-                                                      const ZeroRows zero) {
+                                                      float* __restrict__ part, int per_warp) {
   constexpr int VL = Elem<T>::V;
   constexpr int AHEAD = VEC ? 4 : 8;              // rows in a batch
   constexpr int BATCHES = 3;                      // VEC: batches on their way
@@ -372,14 +472,8 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const RowMap map, const Gr
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // every `every`-th block reduces, so that reads and zeros mix throughout
-  const int sums = map.unit[map.M] * n_strip, turn = blockIdx.x / every;
-  if (blockIdx.x - turn * every != 0 || turn >= sums) {
-    zero_rows(map, G, keys, E, zero, blockIdx.x - min(sums, turn + 1), reinterpret_cast<unsigned char*>(head));
-    return;
-  }
-  const int u = turn / n_strip;
-  const int c = (turn - u * n_strip) * 32 * VL;
+  const int u = blockIdx.x / n_strip;
+  const int c = (blockIdx.x - u * n_strip) * 32 * VL;
   const int m = worker_of(map.unit, map.M, u);
   const int s0 = map.start[m], s1 = map.start[m + 1];
   const int i0 = s0 + ((u - map.unit[m]) * 8 + w) * per_warp;
@@ -531,17 +625,15 @@ void run_embed(cudaStream_t s, const float* table, int64_t V, int64_t E, const v
 
 template <typename T, bool VEC>
 void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map, int per_warp, int64_t longest,
-                      const GradPtrs& G, const Key* keys, const ZeroRows& zero) {
+                      const GradPtrs& G, const Key* keys) {
   const int n_strip = (int)((a.E + 32 * Elem<T>::V - 1) / (32 * Elem<T>::V));
-  const int64_t blocks = (int64_t)map.unit[map.M] * n_strip, zeros = (int64_t)zero.M * zero.groups;
-  const int every = zeros >= blocks ? 2 : 1;
+  const int64_t blocks = (int64_t)map.unit[map.M] * n_strip;
   auto* reduce = k_embed_reduce<T, VEC>;
   const size_t smem = VEC ? 8 * 3 * 4 * 32 * 16 : 0;
   if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)reduce, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   count_launch();
-  launch_pdl(reduce, dim3((unsigned)(blocks + zeros)), dim3(256), smem, s, map, G, keys,
-             reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part, per_warp,
-             every, zero);
+  launch_pdl(reduce, dim3((unsigned)blocks), dim3(256), smem, s, map, G, keys,
+             reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part, per_warp);
   if (longest <= 8 * per_warp) return;   // no run leaves its unit
   count_launch();
   launch_pdl(k_embed_join<T, VEC>, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, map, G, keys, (int)a.E, n_strip,
@@ -555,6 +647,13 @@ RowMap make_map(const int* start, int M, int tile) {
   for (int m = 0; m < M; ++m) map.unit[m + 1] = map.unit[m] + (int)(((int64_t)start[m + 1] - start[m] + tile - 1) / tile);
   return map;
 }
+
+// Chunks of zeros, in entries: 64 KB a block keeps the 256-thread blocks many
+// and short.  k_radix_block's 1024 threads start too slowly for that: four shares
+// an SM, up to 512 KB (4 x 8191 x 1001: 45 us with four, 50 with sixteen; 8 x
+// 50304 x 768 of 4096 tokens each 209 with 512 KB, 231 with 2 MB).
+constexpr int64_t kZeroChunk = 16384;
+constexpr int64_t kZeroMost = 131072;
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -578,55 +677,68 @@ void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start,
   const int N = start[M];
   int64_t longest = 0;
   for (int m = 0; m < M; ++m) longest = longest > start[m + 1] - start[m] ? longest : start[m + 1] - start[m];
-  ZeroRows z{};
-  if (!a.accumulate) {
-    // about 128 KB of table rows a block, at most one row per thread
-    const int64_t fit = 32768 / a.E;
-    z.M = M;
-    z.rows = (int)(fit < 1 ? 1 : fit > 256 ? 256 : fit);
-    z.groups = (int)((a.V + z.rows - 1) / z.rows);
-    z.L = 1;
-    while (z.L < 32 * (z.rows < 8 ? 8 : 1) && z.L * 4 < a.E) z.L <<= 1;
-    z.off = a.off;
-    z.V = a.V;
-  }
+  // the tables' chunks, shared out over the launches of the sort
+  ZeroTables zero{0, 0, 0, a.off, a.V * a.E};
+  int launches = 1, launched = 0;
+  auto with_zeros = [&](int blocks, int64_t chunk) {
+    zero.chunk = (int)chunk;
+    zero.per_table = (int)((zero.size + chunk - 1) / chunk);
+    const int64_t chunks = a.accumulate ? 0 : (int64_t)M * zero.per_table;
+    zero.first = chunks * launched / launches;
+    ++launched;
+    return dim3((unsigned)(blocks + chunks * launched / launches - zero.first));
+  };
   if (N == 0) {
-    if (z.M == 0) return;
-    const RowMap none = make_map(start, M, kSortTile);
+    if (a.accumulate) return;
+    const dim3 grid = with_zeros(0, kZeroChunk);
     count_launch();
-    launch_pdl(k_zero_rows, dim3((unsigned)((int64_t)M * z.groups)), dim3(256), 0, s, none, G, (int)a.E, z);
+    launch_pdl(k_zero_tables, grid, dim3(256), 0, s, G, zero);
     return;
   }
   int at = 0;
   if (longest <= kSortTile) {
     const RowMap tiles = make_map(start, M, kSortTile);
+    const dim3 grid = with_zeros(tiles.unit[M], kZeroChunk);
     count_launch();
-    launch_pdl(a.V < (int64_t(1) << (32 - kPlaceBits)) ? k_sort_tiles<unsigned> : k_sort_tiles<Key>, dim3(tiles.unit[M]),
-               dim3(kSortThreads), 0, s, tiles, a.ids, a.id64, a.V, a.keys[0], a.status);
+    launch_pdl(a.V < (int64_t(1) << (32 - kPlaceBits)) ? k_sort_tiles<unsigned> : k_sort_tiles<Key>, grid,
+               dim3(kSortThreads), 0, s, tiles, a.ids, a.id64, a.V, a.keys[0], a.status, G, zero);
   } else {
     const RowMap tiles = make_map(start, M, kRadixTile);
     int width = 1;   // bits of the ids 0 ... V
     while (a.V >> width) ++width;
     const int digits = (width + kDigitBits - 1) / kDigitBits, bits = (width + digits - 1) / digits;
-    count_launch();
-    launch_pdl(k_radix_count, dim3(tiles.unit[M]), dim3(256), 0, s, tiles, a.ids, a.id64, a.V, bits, digits,
-               a.counts, a.count_set, a.status);
-    for (int k = 0; k < digits; ++k) {
+    if (longest <= (a.accumulate ? kBlockTile / 2 : kBlockTile)) {
+      const size_t smem = block_smem(bits);
+      cudaFuncSetAttribute((const void*)k_radix_block, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      int64_t share = zero.size * M / (num_sms() * 4) / kZeroChunk * kZeroChunk;
+      share = share < kZeroChunk ? kZeroChunk : share > kZeroMost ? kZeroMost : share;
+      const dim3 grid = with_zeros(M, share);
       count_launch();
-      launch_pdl(k_radix_scatter, dim3(tiles.unit[M]), dim3(256), 0, s, tiles, a.ids, a.id64, a.V, k * bits, bits,
-                 k == 0 ? (const Key*)nullptr : (const Key*)a.keys[at ^ 1], a.keys[at],
-                 a.counts + k * a.count_set, k + 1 < digits ? a.counts + (k + 1) * a.count_set : (int*)nullptr);
-      at ^= 1;
+      launch_pdl(k_radix_block, grid, dim3(kBlockThreads), smem, s, tiles, a.ids, a.id64, a.V, bits, digits, a.keys[0],
+                 a.status, G, zero);
+    } else {
+      launches = digits + 1;
+      dim3 grid = with_zeros(tiles.unit[M], kZeroChunk);
+      count_launch();
+      launch_pdl(k_radix_count, grid, dim3(256), 0, s, tiles, a.ids, a.id64, a.V, bits, digits, a.counts, a.count_set,
+                 a.status, G, zero);
+      for (int k = 0; k < digits; ++k) {
+        at = k & 1;
+        grid = with_zeros(tiles.unit[M], kZeroChunk);
+        count_launch();
+        launch_pdl(k_radix_scatter, grid, dim3(256), 0, s, tiles, a.ids, a.id64, a.V, k * bits, bits,
+                   k == 0 ? (const Key*)nullptr : (const Key*)a.keys[at ^ 1], a.keys[at],
+                   a.counts + k * a.count_set, k + 1 < digits ? a.counts + (k + 1) * a.count_set : (int*)nullptr, G, zero);
+      }
     }
-    at ^= 1;
   }
   const int per_warp = embed_per_warp(N, a.E, a.type);
   const RowMap map = make_map(start, M, 8 * per_warp);
   const int vl = a.type == LT_F32 ? 4 : 8;
   const bool vec = a.E % vl == 0 && a.ld % vl == 0 && a.off % 4 == 0 && on16(a.dY);
 #define SM_RUN(T)                                                                     \
-  (vec ? run_embed_reduce<T, true>(s, a, map, per_warp, longest, G, a.keys[at], z)    \
-       : run_embed_reduce<T, false>(s, a, map, per_warp, longest, G, a.keys[at], z))
+  (vec ? run_embed_reduce<T, true>(s, a, map, per_warp, longest, G, a.keys[at])    \
+       : run_embed_reduce<T, false>(s, a, map, per_warp, longest, G, a.keys[at]))
   if (a.type == LT_F32) SM_RUN(float);
   else if (a.type == LT_BF16) SM_RUN(__nv_bfloat16);
   else SM_RUN(__half);
