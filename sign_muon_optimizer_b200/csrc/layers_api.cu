@@ -118,14 +118,16 @@ int norm_blocks(signmuon_t h) { return h->n_sm * 8 + h->M; }
 // workspace layout, in bytes: embed_grad has two key arrays, digit counts and
 // the parts of cut runs, layernorm_grad the blocks' sums, distill the
 // rows' losses and stats
-int64_t embed_units(signmuon_t h, int64_t rows) {
-  const int64_t most = (sm::kFewBlocks + 1) * 256;   // rows that may go in units of 64
-  const int64_t a = (rows < most ? rows : most) / 64, b = rows / 256;
-  return (a > b ? a : b) + h->M + 1;
+// Parts of cut runs: units x columns.  Units of 64 rows are taken where
+// (rows / 256) * strips <= kFewBlocks, with strips >= columns / 256, so that
+// (rows / 64) * columns <= (kFewBlocks + strips) * 1024.
+int64_t embed_parts(signmuon_t h, int64_t rows, int64_t cols) {
+  const int64_t few = std::min(rows / 64 * cols, sm::kFewBlocks * 1024 + 4 * cols + 1024);
+  return std::max(rows / 256 * cols, few) + (h->M + 1) * cols;
 }
 int64_t count_set(signmuon_t h, int64_t rows) { return (rows / sm::kRadixTile + h->M + 1) * sm::kRadixBins; }
 int64_t embed_bytes(signmuon_t h, int64_t rows, int64_t cols) {
-  return 2 * align256(rows * 8) + sm::kRadixSets * count_set(h, rows) * 4 + embed_units(h, rows) * 2 * cols * 4;
+  return 2 * align256(rows * 8) + sm::kRadixSets * count_set(h, rows) * 4 + embed_parts(h, rows, cols) * 2 * 4;
 }
 int64_t norm_bytes(signmuon_t h, int64_t cols) {
   return cols <= SIGNMUON_LAYERNORM_MAX_COLS ? (int64_t)norm_blocks(h) * 2 * cols * 4 : 0;
