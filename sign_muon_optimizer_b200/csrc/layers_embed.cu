@@ -68,10 +68,10 @@ __global__ void __launch_bounds__(256) k_embed(const float* table, int64_t V, in
 // further blocks of its launches zero the tables meanwhile.  Rows with tokens
 // are then written twice; zeroing the others alone, beside the sums, writes every
 // byte once but waits for the sort: 131072 tokens, 8 tables of 50304 x 768, bf16:
-// 259 us against 275 (8192 tokens: 197 against 210); 9001 tokens, 4 tables of
-// 8191 x 1001, fp16: 45 against 55.  Where the tokens outnumber the rows it costs
+// 258 us against 275 (8192 tokens: 180 against 210); 9001 tokens, 4 tables of
+// 8191 x 1001, fp16: 40 against 55.  Where the tokens outnumber the rows it costs
 // a little (8192 tokens, 8 x 1000 x 768, fp32: 28 against 26).
-// Of the 259 us 179 are the sort and zeros (6.9 TB/s), 76 the sums and 7 the join.
+// Of the 258 us 178 are the sort and zeros (6.9 TB/s), 70 the sums and 8 the join.
 // Absent tokens (id < 0, id >= V) get the id kAbsent and sort to the end.
 // ---------------------------------------------------------------------------
 typedef unsigned long long Key;  // id in the upper 32 bits, row in the lower
