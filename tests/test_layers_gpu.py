@@ -130,6 +130,9 @@ def ids_of(kind, n, V, g):
     ("bf16", [700, 9], 3, 9000, "random", 0, False),         # rows zeroed by a whole block
     ("f32", [16639], 300, 4, "zipf", 0, False),              # the last size of small units
     ("f32", [16640], 300, 4, "zipf", 0, False),
+    ("bf16", [40, 0, 3], 700, 77, "random", 0, False),        # tables of several chunks of zeros at odd addresses,
+    ("f32", [3000, 0], 901, 77, "random", 0, False),          # in each form of the sort
+    ("f16", [9000, 0], 1100, 61, "random", 0, False),
     ("f16", [4097, 0, 4096], 500, 6, "random", 0, True),      # borders of the sort's forms
     ("bf16", [4096, 17], 70, 9, "zipf", 1, True),
 ])
