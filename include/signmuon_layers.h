@@ -85,7 +85,7 @@ int signmuon_embed(signmuon_t h, const float* W, int mat, const void* ids, int i
  * tokens are not touched.  Rows of dY with a negative id are not read.
  *   G     host array of M device pointers, float[d], 16-byte aligned.
  * The tokens are sorted by id, so a row's sum is made in registers over its
- * tokens in order, with no atomics.
+ * tokens in order, without floating-point atomics.
  * ---------------------------------------------------------------------- */
 int signmuon_embed_grad(signmuon_t h, int mat, const void* ids, int id_type, const int64_t* rows,
                         float scale, const void* dY, int type, int64_t ld, float* const* G,

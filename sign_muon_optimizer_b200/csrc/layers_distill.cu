@@ -390,7 +390,7 @@ __device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
 // and a second time, from L2, for the gradient, which is written.  8192 x 50304
 // bf16 with 64 entries: 336 us for the call, 310 of them here, 5.3 TB/s of
 // DRAM (818 MB read, as if the second reading were free, and 824 written); loss
-// only, 3001 x 32003 fp16, 33 entries: 46 for the call.  What counts
+// only, 3001 x 32003 fp16, 33 entries: 44 for the call.  What counts
 // is that there are always loads on their way: several blocks on an SM, in
 // different parts of their rows, do better than rows kept in shared memory and
 // loaded a row ahead, of which two fit (8192 x 32003 bf16, 64 entries: 217 us
@@ -406,7 +406,12 @@ template <typename T, int ROW_THREADS>
 constexpr int min_blocks() {
   return ROW_THREADS == 512 ? 3 : ROW_THREADS == 32 ? (Elem<T>::kHalf ? 8 : 9) : (kBlocks - (Elem<T>::kHalf ? 1 : 0)) * (256 / ROW_THREADS);
 }
-constexpr int kAhead = 2;       // packs a thread loads before it uses the first
+// packs a thread loads before it uses the first; the loss alone leaves room for more
+constexpr int kAhead = 2;
+template <int ROW_THREADS, bool GRAD>
+constexpr int first_ahead() {
+  return !GRAD && ROW_THREADS == 128 ? 4 : kAhead;
+}
 template <typename T, int ROW_THREADS, bool GRAD, bool FEW>
 __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 2 : min_blocks<T, ROW_THREADS>())
     k_distill_rows(const RowMap map, const Teacher te, const RowStat* stat, const int* kinds,
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(ROW_THREADS == 32 ? 128 : ROW_THREADS, FEW ? 2
   }
   Running run;
   if (kind != ROW_NONE) {
-    absorb<T, ROW_THREADS, kAhead>(run, v.packs(), v.nv, tid, c, held, GRAD ? hold : 0);
+    absorb<T, ROW_THREADS, first_ahead<ROW_THREADS, GRAD>()>(run, v.packs(), v.nv, tid, c, held, GRAD ? hold : 0);
     if (tid < v.head) run.one(Elem<T>::up(v.z[tid]), c);
     if (v.tail() + tid < V) run.one(Elem<T>::up(v.z[v.tail() + tid]), c);
   }
@@ -620,12 +625,16 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
 // with gradient of 4000 bf16 take 71 / 91 / 135 us with 32 / 128 / 256 threads,
 // of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382; 8192 rows of
 // 50304 bf16 350 with 256 and 324 with 512, of 32003 214 and 238, for which
-// L2 is large enough either way.
+// L2 is large enough either way.  The loss alone does without L2, and better with
+// few threads for longer rows too, as long as there are rows for two rounds of
+// them: 8192 x 32003 fp16 97 us with 128 and 114 with 256, 8192 x 50304 bf16 137
+// and 141, but 1500 x 50304 40 and 36, 4096 x 128256 167 and 164.
 template <typename T, bool GRAD, bool FEW>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   const int64_t row = a.V * (int64_t)sizeof(T);
   if (row <= 16 * 1024) run_rows<T, 32, GRAD, FEW>(s, a, map, te, x);
-  else if (row <= 48 * 1024) run_rows<T, 128, GRAD, FEW>(s, a, map, te, x);
+  else if (row <= 48 * 1024 || (!GRAD && row <= 128 * 1024 && map.start[map.M] >= 2 * num_sms() * min_blocks<T, 128>()))
+    run_rows<T, 128, GRAD, FEW>(s, a, map, te, x);
   else if (row <= 80 * 1024) run_rows<T, 256, GRAD, FEW>(s, a, map, te, x);
   else run_rows<T, GRAD ? 512 : 256, GRAD, FEW>(s, a, map, te, x);
 }

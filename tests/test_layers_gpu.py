@@ -541,6 +541,20 @@ def test_distill_many_rows_with_gaps_and_repeats(V, K, grad, in_place):
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+def test_distill_loss_of_many_long_rows():
+    """Loss only, rows at every alignment, more of them than go at once."""
+    rows = [3000, 1, 199]
+    n, V = sum(rows), 26003
+    opt = handle([(1, 4)], len(rows), n, 4)
+    g = gen(V)
+    Z = (torch.randn(n, V, generator=g, device="cuda") * 2).to(torch.bfloat16)
+    Z[5, 100:] = -float("inf")
+    idx, t = teacher(n, V, 12, g, torch.int64, absent=0.1)
+    idx[5] = torch.arange(12, device="cuda")
+    got = run_distill(opt, Z, idx, t, rows, 1.0, 1.0, False)
+    check_distill(got, f64(Z), idx, t, rows, 1.0, 1.0, torch.bfloat16)
+
+
 def test_distill_loss_only_equals_loss_with_gradient():
     opt = handle([(1, 4)], 3, 40, 4)
     g = gen(41)
