@@ -139,6 +139,9 @@ int signmuon_layernorm_grad(signmuon_t h, const float* W, int gamma, int beta, c
  *   row_loss  device float[rows], may be NULL.
  *   dZ     rows x V of `type`, row stride ldd; may be Z itself (same pointer
  *          and row stride).
+ * Masks may be any finite value too: p is 0 where it is below 2^-126.  Rows whose
+ * largest logit is beyond about 1.1e7 temperature, on either side of zero, take
+ * longer (their logits are read once more, one by one).
  * 1e-18 <= temperature <= 1e18, 1 <= V <= 2^30, 1 <= K; K <= SIGNMUON_DISTILL_MAX_K
  * (E_UNSUPPORTED).
  * ---------------------------------------------------------------------- */

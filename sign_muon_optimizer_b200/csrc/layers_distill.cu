@@ -128,10 +128,12 @@ __device__ __forceinline__ float pack_max(const Pack<__half>& p) {
 
 // A running softmax of y = z c (c = log2 e / T): the maximum m of the logits
 // and the sum s of 2^(z c - R), with the reference R = fl(m c), one fma a term.
-// The rounding of R is common to every term and cancels in p.  R is at least
-// -1e37, so that logits of -inf or of the type's lowest value add 0 to s; rows
-// whose own maximum is out of range are `far` and done over, term by term.
-constexpr float kFar = 1e37f;
+// The rounding of R is common to every term and cancels in p, as long as it is
+// small: within |R| <= 2^24 it is at most 1, but at m c = -1.44e10 it reaches
+// 512, and 2^512 is infinity.  So R is at least -2^24, and masked logits, at
+// -1e10 as well as at -inf, add 0 to s; rows whose own maximum is out of range
+// are `far` and done over, term by term.
+constexpr float kFar = 16777216.f;
 __device__ __forceinline__ float reference(float m, float c) { return fmaxf(m * c, -kFar); }
 
 struct Running {
