@@ -283,6 +283,13 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int i64, int64_t i) 
 #endif  // __CUDACC__
 
 // ---- launch wrappers (host) ------------------------------------------------
+// Lets a kernel be launched with all the dynamic shared memory that its static
+// part leaves, on the current device: what launches of more than 32 KB need.  The
+// limit belongs to the kernel, for every handle and host thread, so it is set
+// once and to the most: lowered to one launch's size it would refuse another
+// thread's larger one.
+void allow_shared(const void* kernel);
+
 constexpr int kSortTile = 2048;   // tokens of a worker that one block sorts
 constexpr int kRadixTile = 2048;  // ... and that a block of the radix sort takes
 constexpr int kRadixBins = 512, kRadixSets = 4;

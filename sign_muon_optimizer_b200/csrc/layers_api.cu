@@ -3,6 +3,9 @@
 #include <algorithm>
 #include <climits>
 #include <initializer_list>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "../../include/signmuon_layers.h"
 #include "ctx.h"
@@ -14,6 +17,20 @@ using sm::aligned16;
 using sm::check_handle;
 using sm::dalloc;
 using sm::fail;
+
+void sm::allow_shared(const void* kernel) {
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> allowed;
+  int dev = 0, most = 0;
+  cudaFuncAttributes own{};
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (allowed.count({kernel, dev})) return;
+  if (cudaFuncGetAttributes(&own, kernel) == cudaSuccess &&
+      cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)own.sharedSizeBytes) == cudaSuccess)
+    allowed.insert({kernel, dev});     // (else the launch reports it)
+}
 
 namespace {
 

@@ -613,7 +613,7 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
     }
     smem += (size_t)hold * 16;
   }
-  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) allow_shared((const void*)kernel);
   const int blocks = (map.start[map.M] + ROWS - 1) / ROWS;
   const int early = num_sms() * resident_per_sm((const void*)kernel, ROWS * ROW_THREADS, smem);
   count_launch();

@@ -630,7 +630,7 @@ void run_embed_reduce(cudaStream_t s, const EmbedGradArgs& a, const RowMap& map,
   const int64_t blocks = (int64_t)map.unit[map.M] * n_strip;
   auto* reduce = k_embed_reduce<T, VEC>;
   const size_t smem = VEC ? 8 * 3 * 4 * 32 * 16 : 0;
-  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)reduce, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) allow_shared((const void*)reduce);
   count_launch();
   launch_pdl(reduce, dim3((unsigned)blocks), dim3(256), smem, s, map, G, keys,
              reinterpret_cast<const T*>(a.dY), a.ld, (int)a.E, n_strip, a.off, a.scale, a.accumulate, a.part, per_warp);
@@ -709,7 +709,7 @@ void launch_embed_grad(cudaStream_t s, const EmbedGradArgs& a, const int* start,
     const int digits = (width + kDigitBits - 1) / kDigitBits, bits = (width + digits - 1) / digits;
     if (longest <= (a.accumulate ? kBlockTile / 2 : kBlockTile)) {
       const size_t smem = block_smem(bits);
-      cudaFuncSetAttribute((const void*)k_radix_block, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      allow_shared((const void*)k_radix_block);
       int64_t share = zero.size * M / (num_sms() * 4) / kZeroChunk * kZeroChunk;
       share = share < kZeroChunk ? kZeroChunk : share > kZeroMost ? kZeroMost : share;
       const dim3 grid = with_zeros(M, share);

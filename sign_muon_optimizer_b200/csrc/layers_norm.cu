@@ -163,7 +163,7 @@ void run_fwd(cudaStream_t s, const FwdArgs& a) {
   constexpr int CH = EPL / Elem<T>::V;
   const size_t smem = VEC ? (size_t)stages(CH, WARPS * 32) * CH * WARPS * 32 * 16 : 0;
   auto* kernel = k_ln_fwd<T, VEC, WPR, EPL>;
-  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) allow_shared((const void*)kernel);
   const int grid = stream_grid((const void*)kernel, WARPS * 32, smem, (a.n + WARPS / WPR - 1) / (WARPS / WPR), 8);
   count_launch();
   launch_pdl(kernel, dim3(grid), dim3(WARPS * 32), smem, s, reinterpret_cast<const T*>(a.X), a.ldx,

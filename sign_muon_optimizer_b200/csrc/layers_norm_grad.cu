@@ -305,7 +305,7 @@ void run_units(cudaStream_t s, const NormGradArgs& a, const int* start, int M, c
   const size_t sums = WIDE ? (size_t)2 * COLS * 4 : (RPB > 1 ? (size_t)RPB * COLS * 4 : 0);
   const size_t smem = ring > sums ? ring : sums;
   auto* kernel = k_ln_bwd<T, VEC, WPR, EPL, FEW>;
-  if (smem > 32 * 1024) cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) allow_shared((const void*)kernel);
   const int N = start[M];
   // one wave of blocks; every worker's rows split into units of equal length
   int64_t want = (int64_t)num_sms() * resident_per_sm((const void*)kernel, WARPS * 32, smem);
