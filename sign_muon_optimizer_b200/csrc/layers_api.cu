@@ -396,7 +396,12 @@ int signmuon_distill(signmuon_t h, const void* Z, int type, int64_t ldz, int64_t
     a.status = h->lay_status;
     NvtxRange range("signmuon distill");
     sm::launch_distill(h->stream, a, start, h->M);
-    CK(h, cudaGetLastError());
+    const cudaError_t launches = cudaGetLastError();
+    if (launches != cudaSuccess) {
+      // the launches that did go may have counted rows, to which the next call would add
+      cudaMemsetAsync(a.count, 0, 2 * sm::kMaxWorkers * sizeof(int), h->stream);
+      CK(h, launches);
+    }
     return SIGNMUON_OK;
   });
 }

@@ -198,9 +198,42 @@ static int limits() {
   return 0;
 }
 
+// A distillation whose n-th launch fails: its first kernel has counted rows, which
+// the next call would add to.
+static int counters() {
+  cleared.clear();
+  signmuon_t h = handle(4, 8, 2000);
+  CHECK(h != nullptr && cleared.size() == 1);
+  const char* from = (const char*)cleared[0].p + sizeof(int);   // behind the status
+  const char* to = (const char*)cleared[0].p + cleared[0].bytes;
+  for (int64_t n : {2, 2000})
+    for (int grad = 0; grad < 2; ++grad) {
+      int before = launches;
+      CHECK(distill(h, SIGNMUON_BF16, 5000, 4, n, grad) == SIGNMUON_OK);
+      const int count = launches - before;
+      CHECK(count == (n == 2 ? 2 : 3));
+      for (int k = 0; k < count; ++k) {
+        before = launches;
+        cleared.clear();
+        fail_at = launches + k;
+        CHECK(distill(h, SIGNMUON_BF16, 5000, 4, n, grad) == SIGNMUON_E_CUDA);
+        CHECK(strstr(signmuon_last_error(h), "made by the test") != nullptr);
+        fail_at = -1;
+        bool all = false;
+        for (const Cleared& c : cleared)
+          all = all || (c.value == 0 && (char*)c.p <= from && (char*)c.p + c.bytes >= to && c.after == launches);
+        CHECK(all || k == 0);
+        CHECK(distill(h, SIGNMUON_BF16, 5000, 4, n, grad) == SIGNMUON_OK);   // and is usable
+      }
+    }
+  signmuon_destroy(h);
+  return 0;
+}
+
 int main(int argc, char** argv) {
   int rc = 2;
   if (argc == 2 && !strcmp(argv[1], "limits")) rc = limits();
+  if (argc == 2 && !strcmp(argv[1], "counters")) rc = counters();
   printf(rc ? "failed\n" : "layer launches ok\n");
   return rc;
 }

@@ -43,3 +43,7 @@ def test_a_kernels_shared_memory_limit_is_never_lowered(program):
     """The limit belongs to the kernel, for all handles and host threads: another
     thread's launch, made ready before it was lowered, would be refused."""
     _run(program, "limits")
+
+
+def test_a_distillation_that_fails_between_its_launches_clears_its_counters(program):
+    _run(program, "counters")
