@@ -624,13 +624,14 @@ void run_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Tea
 }
 
 // Few threads for short rows, so that each has something to load: 16384 rows
-// with gradient of 4000 bf16 take 71 / 91 / 135 us with 32 / 128 / 256 threads,
-// of 16000 bf16 258 / 204 / 244, of 16000 fp32 537 / 433 / 382; 8192 rows of
-// 50304 bf16 350 with 256 and 324 with 512, of 32003 214 and 238, for which
+// with gradient of 4000 bf16 take 73 / 89 / 131 us with 32 / 128 / 256 threads,
+// of 16000 bf16 273 / 202 / 241, of 16000 fp32 551 / 441 / 378; 8192 rows of
+// 50304 bf16 351 with 256 and 325 with 512, of 32003 221 and 246, for which
 // L2 is large enough either way.  The loss alone does without L2, and better with
 // few threads for longer rows too, as long as there are rows for two rounds of
-// them: 8192 x 32003 fp16 97 us with 128 and 114 with 256, 8192 x 50304 bf16 137
-// and 141, but 1500 x 50304 40 and 36, 4096 x 128256 167 and 164.
+// them: 8192 x 32003 fp16 97 us with 128 and 115 with 256, 8192 x 50304 bf16 139
+// and 145, but 1500 x 50304 40 and 38, 4096 x 128256 171 and 168.  (Calls one
+// behind the other on two inputs in turn; with more of them the 325 are 336.)
 template <typename T, bool GRAD, bool FEW>
 void pick_rows(cudaStream_t s, const DistillArgs& a, const RowMap& map, const Teacher& te, const Scratch& x) {
   const int64_t row = a.V * (int64_t)sizeof(T);

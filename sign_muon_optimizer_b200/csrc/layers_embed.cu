@@ -12,7 +12,7 @@ namespace {
 // elements written, one 4 * E-byte table row read per token (from L2 where
 // tokens repeat).  One warp per (row, slab of kSlab columns), so that a short row
 // is one warp's few wide loads and a long one spreads.  131072 tokens of a
-// 50304 x 768 table to bf16: 59 us, 0.93 of the time its DRAM bytes need; 8
+// 50304 x 768 table to bf16: 60 us, of which its DRAM bytes need 0.90; 8
 // tokens: 2.4 us on the device, of which the launch is nearly all.
 // ---------------------------------------------------------------------------
 constexpr int kSlab = 1024;
@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_tiles(const RowMap map, c
 // and the count take about 18 us for 8193 to 131072 tokens: latency, three
 // launches in a row.
 // The first counts are made by k_radix_count; each scatter makes the next
-// digit's by (integer) atomics.  There is a set of counts per digit.  Absent
+// digit's by (integer) atomics.  There is a set of counts per digit; a scatter
+// block reads all of its worker's, which is nothing at 131072 tokens, but grows with
+// the square of a worker's tokens (2^20: 0.5 GB a digit; 2^24: 130 GB).  Absent
 // tokens sort as id V.
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 static_assert(kBins == kRadixBins && kRadixSets * kDigitBits >= 31, "the workspace has a set of counts per digit");

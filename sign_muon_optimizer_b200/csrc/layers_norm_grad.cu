@@ -18,7 +18,7 @@ constexpr int kStages = 3;
 // Rows on 16-byte boundaries come in through asynchronous copies, kStages rows
 // ahead, into slots that only the copying thread reads.
 // Should be bound by the bytes (X and dY read once, dX written once), and takes
-// 166 us for 32768 x 4096 bf16, 4.9 TB/s, and 122 for 131072 x 768: the weights,
+// 166 us for 32768 x 4096 bf16, 4.9 TB/s, and 100 for 131072 x 768: the weights,
 // the sums and the row take 120 registers, so 16 warps fit an SM and issue in
 // half of its cycles, each row with a barrier in its middle.  More stages, fewer
 // elements a lane and a shorter reduction of the two row sums all take the same
@@ -26,7 +26,8 @@ constexpr int kStages = 3;
 // and converting 16-bit values in pairs to 166.
 // The longest rows (EPL = 32) leave no registers for the sums and the weights
 // and no shared memory for the slots: their sums are in shared memory, and the
-// second pass loads them again (from L2).
+// second pass loads them again (from L2).  One such block fits an SM, and nothing
+// is loaded ahead: 4096 x 16384 bf16 takes 232 us where the bytes need 61.
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC, int WPR, int EPL, bool FEW>
 __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256, (WPR > 8 ? 1 : 2) + (EPL <= 8 ? 1 : 0))
@@ -350,7 +351,7 @@ void run_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, con
 // The fewest warps that hold a row at 16 elements a lane; without the
 // asynchronous copies at 8, which lets a third block wait on its loads too
 // (30000 x 1001 fp32 86 us instead of 107, 8000 x 4001 bf16 68 instead of 80;
-// with the copies 32768 x 4096 bf16 takes 216 us at 8 and 153 at 16).  Above
+// with the copies 32768 x 4096 bf16 takes 226 us at 8 and 166 at 16).  Above
 // 16 warps at 16, 32.
 template <typename T, bool VEC>
 void pick_bwd(cudaStream_t s, const NormGradArgs& a, const int* start, int M, const GradPtrs& G) {
